@@ -265,6 +265,78 @@ int q4_linear_w4a8_ws(const int8_t* xq, const float* scale_a, int32_t m, const q
                       int32_t* dev_status, void* stream);
 
 /*
+ * q8_linear_w8a8 -- INT8 activations x INT8 weights, INT32 accumulation, one rescale at the end.
+ * Source: the W4A8 page §2.3 (8-bit products into INT32, rescaled by scale_w * scale_a) and §5.1 (projections
+ * that do not stand 4-bit weights keep 8); here with one weight scale per output channel.
+ *   acc[m][n] = sum_k xq[m][k] * wq[n][k]                                   (exact int32)
+ *   y[m][n]   = (float(acc) * scale_w[n]) * scale_a[m] + bias[n]            (fp32, each step rounded to nearest)
+ * xq [m][k] int8 and scale_a [m] fp32 as act_quant_per_token makes them; wq [n][k] int8 and scale_w [n] fp32 (16-bit
+ * weights quantized by the same call: a row of W is one channel); bias [n] fp32 or NULL; y [m][n] fp32 or
+ * bf16 (round to nearest even of the fp32 result).  m >= 0, n >= 0, 16 <= k <= Q8_MAX_K, k % 16 == 0 (rows start
+ * on 16 bytes; Q8_MAX_K is the longest sum of products of -128 .. 127 that int32 holds).  xq, wq and y 16-byte
+ * aligned, the fp32 arrays 4-byte aligned.  The result does not depend on how the sum is split: it is exact.
+ * dev_status: Q4_ERR_TIMEOUT when a bounded wait ran out.
+ */
+#define Q8_MAX_K 131056
+int q8_linear_w8a8(const int8_t* xq, const float* scale_a, int32_t m, const int8_t* wq, const float* scale_w,
+                   int32_t n, int32_t k, const float* bias, void* y, int32_t out_dtype, int32_t* dev_status,
+                   void* stream);
+
+/*
+ * q8_linear_w8a8_gated -- the gated half of a feed-forward block on INT8 codes: both projections, the
+ * activation and the product in one kernel; neither projection is written to memory.
+ * Source: "高效大语言模型推理实践：INT4量化与MoE架构的融合探索" MoE架构设计 (the FFN is SwiGLU); the W4A8 page
+ * §2.3 and §5.1 as q8_linear_w8a8.
+ *   g[m][i] = (float(sum_k xq[m][k] * wq_gate[i][k]) * scale_gate[i]) * scale_a[m], u likewise from wq_up;
+ *   h[m][i] = act(g) * u in fp32;  Q8_ACT_SILU: g / (1 + e^-g);
+ *             Q8_ACT_GELU: g / (1 + e^(-2 z)) with z = sqrt(2/pi) * (g + 0.044715 g^3) (the tanh form of GELU).
+ * wq_gate, wq_up [n][k] int8 (n the intermediate size), scale_gate, scale_up [n] fp32; h [m][n] fp32 or bf16.
+ * For the down projection a caller quantizes h with act_quant_per_token.  Sizes and alignment as
+ * q8_linear_w8a8.
+ */
+enum { Q8_ACT_SILU = 0, Q8_ACT_GELU = 1 };
+int q8_linear_w8a8_gated(const int8_t* xq, const float* scale_a, int32_t m, const int8_t* wq_gate,
+                         const float* scale_gate, const int8_t* wq_up, const float* scale_up, int32_t n, int32_t k,
+                         int32_t act, void* h, int32_t out_dtype, int32_t* dev_status, void* stream);
+
+/*
+ * block_norm -- what stands between two blocks of a layer stack, in one pass over the rows: the norm after a
+ * block, its gate, the residual update with its scales, the norm before the next block, and the INT8 codes for
+ * the next block's first product.
+ * Source: the W4A8 page §3.1 (per-token codes of the rows a product takes); the norms are the RMS norms
+ * of the LLaMA-shaped layers whose linears this library serves.
+ *   rstd(v) = fp32 of (sum v^2 / H + eps)^(-1/2), the sum and the root in fp64;
+ *   b  = (x * rstd(x)) * post_w          (b = x when post_w is NULL)
+ *   b  = (b * branch_scale) * gate       (no gate factor when gate is NULL)
+ *   r' = residual * res_scale + b        (r' = b without residual, residual * res_scale without x)
+ *   n  = (r' * rstd(r')) * pre_w         (no factor when pre_w is NULL)
+ * Each product and sum above is one fp32 operation rounded to nearest, in that order; r' is rounded to its type
+ * only where it is stored (n comes from the fp32 values).  xq, scale_a = what act_quant_per_token gives for
+ * the rows n as y_dtype holds them, bit for bit.
+ *   x [T][H], residual [T][H] (either may be NULL, not both; a gate or post_w needs x);
+ *   post_w, pre_w [H] of w_dtype; gate [gate_rows][H]: row t / (T / gate_rows) scales token t (gate_rows divides T;
+ *   1: one gate for all); residual_out [T][H] of residual_dtype; y [T][H] of y_dtype; xq [T][H] int8 with
+ *   scale_a [T] fp32.  Each output is optional (at least one; xq and scale_a together).  residual_out
+ *   and y may each replace x or residual when the elements have the same size; an output that overlaps an input
+ *   or another output in any other way is refused (Q4_ERR_UNSUPPORTED).  Every dtype is Q4_F32, Q4_BF16 or Q4_F16;
+ *   1 <= H <= Q4_BLOCK_NORM_MAX_H; eps >= 0 and finite.  Arrays are aligned to their elements; with H % 8 == 0 and
+ *   every array on 16 bytes the kernel uses 16-byte accesses.
+ * dev_status: Q4_ERR_NONFINITE when a row whose codes are wanted holds a non-finite n (its scale is then not finite).
+ */
+enum { Q4_F32 = 0, Q4_BF16 = 1, Q4_F16 = 2 };
+#define Q4_BLOCK_NORM_MAX_H 32768
+typedef struct q4_block_norm {
+    const void *x, *residual, *post_w, *gate, *pre_w;
+    void *residual_out, *y;
+    int8_t* xq;
+    float* scale_a;
+    int32_t x_dtype, residual_dtype, w_dtype, gate_dtype, y_dtype;
+    int32_t gate_rows;
+    float eps, res_scale, branch_scale;
+} q4_block_norm;
+int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t* dev_status, void* stream);
+
+/*
  * moe_q4_workspace_size -- bytes of device workspace moe_q4_forward needs for these sizes.
  */
 size_t moe_q4_workspace_size(int32_t T, int32_t H, int32_t I, int32_t E, int32_t topk);

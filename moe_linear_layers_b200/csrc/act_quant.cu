@@ -18,19 +18,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ int code8(float x, float s, float r, bool exact_div)
-{
-    float q;
-    if (exact_div) {
-        q = x / s;
-    } else {
-        const float t = x * r;
-        const float e = fmaf(-s, t, x);
-        q = fmaf(e, r, t);
-    }
-    return (int)fminf(fmaxf(rintf(q), -128.0f), 127.0f);
-}
-
 // low / high 16-bit value of a word as fp32
 template <bool F16> __device__ __forceinline__ float lo16(uint32_t w)
 {
@@ -51,8 +38,8 @@ __device__ __forceinline__ uint2 code_word(const uint4& v, float s, float r, boo
     uint32_t packed[2] = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const int qa = code8(lo16<F16>(e[j]), s, r, exact_div);
-        const int qb = code8(hi16<F16>(e[j]), s, r, exact_div);
+        const int qa = q4_code8(lo16<F16>(e[j]), s, r, exact_div);
+        const int qb = q4_code8(hi16<F16>(e[j]), s, r, exact_div);
         packed[j / 2] |= ((uint32_t)(qa & 0xFF) | ((uint32_t)(qb & 0xFF) << 8)) << (16 * (j & 1));
     }
     return make_uint2(packed[0], packed[1]);

@@ -64,6 +64,32 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) { return __uint_
 __device__ __forceinline__ uint32_t h2_as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u32_as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
+// INT8 code clamp(rne(x / s), -128, 127) with s > 0; r = RN(1/s).  The quotient is formed without a division
+// (see act_quant.cu: correctly rounded while s >= 2^-100); exact_div takes the division itself.
+__device__ __forceinline__ int q4_code8(float x, float s, float r, bool exact_div)
+{
+    float q;
+    if (exact_div) {
+        q = x / s;
+    } else {
+        const float t = x * r;
+        const float e = fmaf(-s, t, x);
+        q = fmaf(e, r, t);
+    }
+    return (int)fminf(fmaxf(rintf(q), -128.0f), 127.0f);
+}
+
+// Programmatic dependent launch: a kernel launched with q4_launch_pdl may start while the previous kernel on
+// the stream still runs; q4_pdl_start lets the next one start in turn and waits for the previous one's
+// completion.  Memory another kernel may have written (or may still read) is touched only after it.
+__device__ __forceinline__ void q4_pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void q4_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void q4_pdl_start()
+{
+    q4_pdl_trigger();
+    q4_pdl_wait();
+}
+
 // Host side: error mapping for launches.  The last CUDA error is kept per host thread for
 // q4_last_cuda_error_string().
 void q4_record_cuda_error(cudaError_t e);
@@ -76,6 +102,22 @@ static inline int q4_cuda_status(cudaError_t e)
 }
 
 static inline int q4_launch_status() { return q4_cuda_status(cudaGetLastError()); }
+
+template <typename... P, typename... A>
+static inline int q4_launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return q4_cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
+}
 
 static inline bool q4_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,0 +1,37 @@
+// Shared by the INT8 x INT8 (W8A8) kernels: the problem, the rescale and the gated activation.
+#pragma once
+
+#include "q4_common.cuh"
+
+namespace w8 {
+
+struct Problem {
+    const int8_t* xq;        // [m][k]
+    const float* scale_a;    // [m]
+    const int8_t* w0;        // [n][k]: the weights, or the gate's
+    const float* scale_0;    // [n]
+    const int8_t* w1;        // gated: up's
+    const float* scale_1;
+    const float* bias;       // [n] or NULL (plain only)
+    void* y;                 // [m][n]
+    int m, n, k;
+    int out_bf16;
+    int act;                 // gated: Q8_ACT_*
+    int32_t* status;
+};
+
+// acc is exact; fp32 rounds it once (to 2^-24), then each factor once
+__device__ __forceinline__ float rescale(int acc, float sw, float sa) { return __fmul_rn(__fmul_rn((float)acc, sw), sa); }
+
+// v / (1 + e^-z).  __expf and __fdividef are within a few fp32 ulp for the |z| whose result is not negligible; z so
+// negative that e^-z leaves fdividef's range (above 2^126) gives 0, off by less than |v| * 2^-126.
+__device__ __forceinline__ float logistic_times(float v, float z) { return __fdividef(v, 1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float gated(float g, float u, int act)
+{
+    // 2 sqrt(2/pi) = 1.5957691..., times 0.044715 = 0.0713548...
+    const float z = act == Q8_ACT_SILU ? g : g * fmaf(0.0713548163f * g, g, 1.5957691216f);
+    return logistic_times(g, z) * u;
+}
+
+}  // namespace w8

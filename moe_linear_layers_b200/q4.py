@@ -32,6 +32,8 @@ Q4_ERR_TIMEOUT = -8
 Q4_ERR_BOUNDS = -9
 Q4_OUT_F32 = 0
 Q4_OUT_BF16 = 1
+Q8_MAX_K = 131056
+Q4_BLOCK_NORM_MAX_H = 32768
 
 EXPORTED = ("q4_status_string", "q4_version", "q4_build_flags", "q4_last_cuda_error_string", "q4_quantize_pack", "q4_linear_w4a16", "q4_linear_w4a16_max_gemv_m",
             "q4_linear_w4a16_grouped", "q4_linear_w4a16_swiglu",
@@ -40,7 +42,8 @@ EXPORTED = ("q4_status_string", "q4_version", "q4_build_flags", "q4_last_cuda_er
             "act_quant_per_token_f16", "moe_q4_workspace_size_a8", "moe_q4_forward_a8", "moe_q4_forward_classes",
             "moe_q4_forward_range", "q4_linear_w4a16_chain_sync_bytes", "q4_linear_w4a16_chain",
             "moe_q4_route_workspace_size", "moe_q4_route", "moe_q4_rows_workspace_size", "moe_q4_forward_rows",
-            "moe_q4_combine", "q4_linear_workspace_size", "q4_linear_w4a16_ws", "q4_linear_w4a8_ws")
+            "moe_q4_combine", "q4_linear_workspace_size", "q4_linear_w4a16_ws", "q4_linear_w4a8_ws",
+            "q8_linear_w8a8", "q8_linear_w8a8_gated", "block_norm")
 Q4_MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -51,6 +54,14 @@ class q4_weight(ctypes.Structure):
 
 
 _i32, _p, _sz = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+
+
+class q4_block_norm(ctypes.Structure):
+    _fields_ = [(f, _p) for f in ("x", "residual", "post_w", "gate", "pre_w", "residual_out", "y", "xq", "scale_a")] + \
+               [(f, _i32) for f in ("x_dtype", "residual_dtype", "w_dtype", "gate_dtype", "y_dtype", "gate_rows")] + \
+               [(f, ctypes.c_float) for f in ("eps", "res_scale", "branch_scale")]
+
+
 _lib.q4_status_string.restype = ctypes.c_char_p
 _lib.q4_status_string.argtypes = [ctypes.c_int]
 _lib.q4_version.restype = ctypes.c_int
@@ -101,6 +112,9 @@ _lib.moe_q4_forward_rows.argtypes = [_p, _i32, _i32, _p, _i32, _p, _i32, ctypes.
 _lib.moe_q4_combine.argtypes = [_p, _i32, _i32, _p, _p, _i32, _i32, _p, _i32, _p, _p]
 _lib.moe_q4_forward_noalloc.argtypes = [_p, _i32, _i32, _p, _p, _i32, _i32, ctypes.POINTER(q4_weight), _i32, _p,
                                         _i32, _p, _p, _p, _p, _p, _p, _p]
+_lib.q8_linear_w8a8.argtypes = [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p]
+_lib.q8_linear_w8a8_gated.argtypes = [_p, _p, _i32, _p, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p]
+_lib.block_norm.argtypes = [ctypes.POINTER(q4_block_norm), _i32, _i32, _p, _p]
 
 
 class Q4Error(RuntimeError):
@@ -496,6 +510,179 @@ def q4_linear_w4a8(xq: torch.Tensor, scale_a: torch.Tensor, w: Q4Weight, out_dty
                                   _ptr(workspace), workspace.numel() if workspace is not None else 0,
                                   _ptr(dev_status), _stream(stream)), "q4_linear_w4a8")
     return y
+
+
+# ---------------------------------------------------------------------------------------------- #
+# INT8 x INT8 products, their gated form, and the norms between blocks
+# ---------------------------------------------------------------------------------------------- #
+
+def _same(t, dtype, device, shape, name):
+    """A contiguous tensor of one dtype and shape on `device`."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
+    return t.data_ptr()
+
+
+def _status(t, device):
+    """The caller's status word (nullable): an int32 tensor on the inputs' device."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.numel() < 1:
+        raise TypeError("dev_status must be a torch.int32 tensor of one value")
+    if t.device != device:
+        raise ValueError(f"dev_status is on {t.device}, the inputs on {device}")
+    return t.data_ptr()
+
+
+def _call(what, fn, args, device, stream, made, used):
+    """fn(*args, stream) on the inputs' device.  A call on a stream other than the device's current one marks the
+    tensors it was given and those it made as in use there (see _hold)."""
+    if stream is None:
+        if device.index == _current_device():
+            _check(fn(*args, _raw_current_stream(device.index)), what)
+            return
+        with torch.cuda.device(device):
+            _check(fn(*args, _raw_current_stream(device.index)), what)
+        return
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the inputs on {device}")
+    with torch.cuda.device(device):
+        _hold(stream, *made, *used)
+        _check(fn(*args, stream.cuda_stream), what)
+
+
+def _w8_rows(xq, scale_a, wq, name):
+    """Check the codes of a W8A8 call: xq int8 [..][k] on a GPU, scale_a one per row, wq int8 [n][k].  Returns m, n, k."""
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
+        raise ValueError(f"{name} must be an int8 tensor [n][k]")
+    _dev(xq, torch.int8, "xq")
+    n, k = wq.shape
+    if xq.dim() < 1 or xq.shape[-1] != k:
+        raise ValueError(f"xq has rows of {tuple(xq.shape)[-1:]}, {name} of {k} codes")
+    m = xq.numel() // k if k else 0
+    _numel(_dev(scale_a, torch.float32, "scale_a"), m, "scale_a")
+    if scale_a.device != xq.device:
+        raise ValueError(f"scale_a is on {scale_a.device}, xq on {xq.device}")
+    return m, n, k
+
+
+def q8_linear_w8a8(xq: torch.Tensor, scale_a: torch.Tensor, wq: torch.Tensor, scale_w: torch.Tensor,
+                   bias: torch.Tensor | None = None, out_dtype=torch.float32, y: torch.Tensor | None = None,
+                   dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[m][n] = (xq[m][k] . wq[n][k]^T) * scale_w[n] * scale_a[m] (+ bias[n]) with an exact INT32 sum: INT8 codes and
+    per-token scales as act_quant_per_token makes them, INT8 weights with one scale per output channel (the
+    same call on the rows of a 16-bit weight makes those).  k % 16 == 0; fp32 or bf16 output."""
+    m, n, k = _w8_rows(xq, scale_a, wq, "wq")
+    dev = xq.device
+    if y is None:
+        y = torch.empty((m, n), dtype=out_dtype, device=dev)
+    args = (xq.data_ptr(), scale_a.data_ptr(), m, _same(wq, torch.int8, dev, (n, k), "wq"),
+            _same(scale_w, torch.float32, dev, (n,), "scale_w"), n, k,
+            None if bias is None else _same(bias, torch.float32, dev, (n,), "bias"), y.data_ptr(), _out(y, (m, n), dev),
+            _status(dev_status, dev))
+    _call("q8_linear_w8a8", _lib.q8_linear_w8a8, args, dev, stream, (y,), (xq, scale_a, wq, scale_w, bias, dev_status))
+    return y
+
+
+Q8_ACTS = {"silu": 0, "gelu": 1}
+
+
+def q8_linear_w8a8_gated(xq: torch.Tensor, scale_a: torch.Tensor, wq_gate: torch.Tensor, scale_gate: torch.Tensor,
+                         wq_up: torch.Tensor, scale_up: torch.Tensor, act: str = "silu", out_dtype=torch.float32,
+                         h: torch.Tensor | None = None, dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h[m][n] = act(g) * u, g and u the q8_linear_w8a8 products of the same codes with the gate and up weights, in
+    one kernel.  act: "silu" or "gelu" (its tanh form)."""
+    if act not in Q8_ACTS:
+        raise ValueError(f"act must be one of {tuple(Q8_ACTS)}, got {act!r}")
+    m, n, k = _w8_rows(xq, scale_a, wq_gate, "wq_gate")
+    dev = xq.device
+    if h is None:
+        h = torch.empty((m, n), dtype=out_dtype, device=dev)
+    args = (xq.data_ptr(), scale_a.data_ptr(), m, _same(wq_gate, torch.int8, dev, (n, k), "wq_gate"),
+            _same(scale_gate, torch.float32, dev, (n,), "scale_gate"), _same(wq_up, torch.int8, dev, (n, k), "wq_up"),
+            _same(scale_up, torch.float32, dev, (n,), "scale_up"), n, k, Q8_ACTS[act], h.data_ptr(), _out(h, (m, n), dev, "h"),
+            _status(dev_status, dev))
+    _call("q8_linear_w8a8_gated", _lib.q8_linear_w8a8_gated, args, dev, stream, (h,),
+          (xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, dev_status))
+    return h
+
+
+_NORM_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _norm_rows(t, shape, device, name):
+    """A contiguous fp32, bf16 or fp16 tensor of that shape; returns its pointer and dtype code."""
+    dt = _NORM_DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dt is None:
+        raise TypeError(f"{name} must be a torch.float32, torch.bfloat16 or torch.float16 CUDA tensor")
+    return _same(t, t.dtype, device, shape, name), dt
+
+
+def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: torch.Tensor | None, post_w: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, eps: float = 1e-5, res_scale: float = 1.0, branch_scale: float = 1.0,
+               out_dtype=torch.bfloat16, quant: bool = False, want_y: bool = True, want_residual: bool = True,
+               residual_out: torch.Tensor | None = None, y: torch.Tensor | None = None, xq: torch.Tensor | None = None,
+               scale_a: torch.Tensor | None = None, dev_status: torch.Tensor | None = None, stream=None):
+    """The boundary between two blocks: b = norm(x) * post_w (b = x without post_w); r = res_scale * residual +
+    gate * branch_scale * b; n = norm(r) * pre_w.  x: the block's output [T][H] (None: only the residual is scaled
+    and normed); residual [T][H] (None: r = the gated b); gate None, [H], or [G][H] (each row for T / G consecutive
+    tokens).  Returns (r, n, xq, scale_a): r in the residual's dtype (x's without one; None unless want_residual), n in
+    out_dtype (None unless want_y), and with quant the INT8 codes and scales act_quant_per_token gives for n (else
+    None, None).  residual_out may be residual itself (in place).  fp32, bf16 or fp16 throughout; post_w and pre_w of
+    one dtype."""
+    lead = x if x is not None else residual
+    if not isinstance(lead, torch.Tensor) or not lead.is_cuda or lead.dim() != 2:
+        raise TypeError("x (or residual) must be a CUDA tensor [T][H]")
+    T, H = shape = lead.shape
+    dev = lead.device
+    if T == 0:
+        gate = None
+    d = q4_block_norm(eps=eps, res_scale=res_scale, branch_scale=branch_scale, gate_rows=1)
+    if x is not None:
+        d.x, d.x_dtype = _norm_rows(x, shape, dev, "x")
+    if residual is not None:
+        d.residual, d.residual_dtype = _norm_rows(residual, shape, dev, "residual")
+    elif x is not None:
+        d.residual_dtype = d.x_dtype
+    if pre_w is not None:
+        d.pre_w, d.w_dtype = _norm_rows(pre_w, (H,), dev, "pre_w")
+    if post_w is not None:
+        if pre_w is not None and pre_w.dtype != post_w.dtype:
+            raise TypeError("post_w and pre_w must have the same dtype")
+        d.post_w, d.w_dtype = _norm_rows(post_w, (H,), dev, "post_w")
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2) or (gate.dim() == 2 and (gate.shape[0] < 1 or T % gate.shape[0])):
+            raise ValueError(f"gate must be [H] or [G][H] with G a divisor of the {T} tokens")
+        d.gate, d.gate_dtype = _norm_rows(gate, (*gate.shape[:-1], H), dev, "gate")
+        d.gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+    r_dtype = residual.dtype if residual is not None else x.dtype
+    if want_residual:
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=r_dtype, device=dev)
+        d.residual_out = _same(residual_out, r_dtype, dev, shape, "residual_out")
+    else:
+        residual_out = None
+    d.y_dtype = _NORM_DTYPES.get(out_dtype if y is None or not want_y else y.dtype, -1)
+    if want_y:
+        if y is None:
+            y = torch.empty(shape, dtype=out_dtype, device=dev)
+        d.y, d.y_dtype = _norm_rows(y, shape, dev, "y")
+    else:
+        y = None
+    if quant:
+        xq = torch.empty(shape, dtype=torch.int8, device=dev) if xq is None else xq
+        scale_a = torch.empty((T,), dtype=torch.float32, device=dev) if scale_a is None else scale_a
+        d.xq = _same(xq, torch.int8, dev, shape, "xq")
+        d.scale_a = _same(scale_a, torch.float32, dev, (T,), "scale_a")
+    else:
+        xq = scale_a = None
+    _call("block_norm", _lib.block_norm, (ctypes.byref(d), T, H, _status(dev_status, dev)), dev, stream,
+          (residual_out, y, xq, scale_a), (x, residual, post_w, gate, pre_w, dev_status))
+    return residual_out, y, xq, scale_a
 
 
 def q4_selftest_bounded_wait(which: int, limit_us: int, dev_status: torch.Tensor, stream=None) -> None:
