@@ -1,6 +1,20 @@
 // Entry points of the INT8 x INT8 (W8A8) products: argument checks and the choice of kernel by size.
 #include "w8a8_common.cuh"
+#include "w8a8_ptx.cuh"
 
+PFN_cuTensorMapEncodeTiled_v12000 w8::tensor_map_encoder()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* f = nullptr;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+    }();
+    return fn;
+}
+
+int w8a8_gemm_launch(const w8::Problem& p, cudaStream_t s);
 int w8a8_small_launch(const w8::Problem& p, cudaStream_t s);
 
 namespace {
@@ -14,7 +28,7 @@ int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
     if (!q4_aligned16(p.xq) || !q4_aligned16(p.w0) || !q4_aligned16(p.w1) || !q4_aligned16(p.y) ||
         (((uintptr_t)p.scale_a | (uintptr_t)p.scale_0 | (uintptr_t)p.scale_1 | (uintptr_t)p.bias) & 3u))
         return Q4_ERR_ALIGN;
-    return w8a8_small_launch(p, s);
+    return p.m <= 64 ? w8a8_small_launch(p, s) : w8a8_gemm_launch(p, s);
 }
 
 }  // namespace

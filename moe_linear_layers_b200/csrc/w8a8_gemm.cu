@@ -1,0 +1,269 @@
+// W8A8 products for many tokens: int8 tcgen05 MMAs on CTA pairs.
+//
+// A pair of CTAs (cluster of 2, cta_group::2) owns a tile of 256 tokens x 256 weight rows: each CTA brings its own 128
+// token rows and 128 of the weight rows into shared memory (TMA, 128-byte swizzle, K-major), the pair's
+// MMA (M 256, N 256, K 32) reads both halves, and each CTA's TMEM receives its 128 token rows x 256 int32 sums.
+// Per 128 codes of K a CTA thus loads 32 KB for 4 MMAs of 128 cycles (64 bytes a cycle; a lone CTA with a 128 x 256
+// tile would need 96).  Gated: the first CTA's weight rows are the gate's, the second's the same rows of up, so a
+// thread finds a token's g and u in columns c and 128 + c of its TMEM lane and h needs no exchange.
+//
+// The whole sum over K stays in the int32 accumulators (exact), so the epilogue touches each output once.
+// Two accumulators (2 x 256 TMEM columns): the epilogue of one tile runs under the MMAs of the next.  Persistent: one
+// pair per two SMs walks the tiles, tokens fastest, so that concurrent pairs share weight rows in L2.
+//
+// Warps (12): 0 TMA producer, 1 MMA issuer (leader CTA only), 2 TMEM owner, 4-11 epilogue (two warps per TMEM lane
+// quarter, each half of the columns).  Every wait is bounded (Q4_ERR_TIMEOUT).
+#include "tc_ptx.cuh"
+#include "w8a8_common.cuh"
+#include "w8a8_ptx.cuh"
+
+namespace {
+
+using w8::Problem;
+
+constexpr int BM = 128;                 // token rows a CTA
+constexpr int BNC = 128;                // weight rows a CTA loads
+constexpr int BN = 2 * BNC;             // accumulator columns
+constexpr int BK = 128;                 // codes of K a stage
+constexpr int kStages = 5;
+constexpr int kStageBytes = (BM + BNC) * BK;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kStageOut = 4096;         // output staging bytes an epilogue warp: 32 rows x (2 x 64 or 1 x 128) bytes
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];   // full: the leader's (both CTAs' copies); empty: each CTA's
+    uint64_t acc_full[2], acc_empty[2];       // acc_full: each CTA's; acc_empty: the leader's (both CTAs' epilogues)
+    uint64_t done;
+    uint32_t tmem;
+    int abort_flag;
+    float sw[BN], bias[BN];                   // the tile's channel scales (gated: gate's, up's) and biases
+};
+
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + (int)sizeof(Shared);
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct Grid {
+    int tiles_m, tiles;
+    int tma_out;    // rows of y start on 16 bytes: stored by TMA
+};
+
+template <bool GATED, bool OUT32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+                 const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_y, const Problem p,
+                 const Grid g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* out_stage = smem + kStages * kStageBytes;
+    Shared* sh = reinterpret_cast<Shared*>(out_stage + kEpiWarps * kStageOut);
+    volatile int* abort_flag = &sh->abort_flag;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = w8::cluster_rank();
+    const int kblocks = (p.k + BK - 1) / BK;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    constexpr int ROWS = GATED ? BNC : BN;   // weight rows (of each matrix) a tile covers
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; i++) {
+            tc::mbar_init(&sh->full[i], 1);
+            tc::mbar_init(&sh->empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            tc::mbar_init(&sh->acc_full[i], 1);
+            tc::mbar_init(&sh->acc_empty[i], 2 * kEpiWarps);
+        }
+        tc::mbar_init(&sh->done, 1);
+        sh->abort_flag = 0;
+        tc::fence_mbar_init();
+        tc::tma_prefetch_desc(&tm_x);
+        tc::tma_prefetch_desc(&tm_w0);
+    }
+    if (warp == 2) w8::tmem_alloc_pair(&sh->tmem, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    w8::cluster_sync();       // both CTAs' barriers are initialised before either is signalled
+    tc::fence_after_sync();
+    const uint32_t tbase = sh->tmem;
+    q4_pdl_start();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = first; t < g.tiles && ok; t += step) {
+                const int m0 = (t % g.tiles_m) * (2 * BM) + (int)rank * BM;
+                const int n0 = (t / g.tiles_m) * ROWS + (GATED ? 0 : (int)rank * BNC);
+                const CUtensorMap* mw = GATED && rank ? &tm_w1 : &tm_w0;
+                for (int kb = 0; kb < kblocks; kb++, it++) {
+                    const int s = it % kStages;
+                    if (!(ok = tc::mbar_wait(&sh->empty[s], ((it / kStages) & 1) ^ 1, p.status, abort_flag))) break;
+                    uint8_t* dst = smem + s * kStageBytes;
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&sh->full[s], 2 * kStageBytes);
+                    const uint32_t bar = w8::map_to_rank(&sh->full[s], 0);
+                    w8::tma_load_pair(dst, &tm_x, bar, kb * BK, m0);
+                    w8::tma_load_pair(dst + BM * BK, mw, bar, kb * BK, n0);
+                }
+            }
+            if (!ok) w8::pause_ns(100000000ull);   // given up: let the copies in flight land before the CTA leaves
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = w8::idesc_s8(2 * BM, BN);
+            uint32_t it = 0, tl = 0;
+            bool ok = true;
+            for (int t = first; t < g.tiles && ok; t += step, tl++) {
+                const uint32_t b = tl & 1;
+                if (!(ok = tc::mbar_wait(&sh->acc_empty[b], ((tl >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+                tc::fence_after_sync();
+                for (int kb = 0; kb < kblocks; kb++, it++) {
+                    const int s = it % kStages;
+                    if (!(ok = tc::mbar_wait(&sh->full[s], (it / kStages) & 1, p.status, abort_flag))) break;
+                    tc::fence_after_sync();
+                    const uint32_t a = tc::smem_u32(smem + s * kStageBytes);
+                    const uint64_t ad = tc::smem_desc_sw128(a), bd = tc::smem_desc_sw128(a + BM * BK);
+#pragma unroll
+                    for (int i = 0; i < BK / 32; i++)
+                        w8::mma_i8_pair(tbase + b * BN, ad + 2 * i, bd + 2 * i, idesc, kb > 0 || i > 0);
+                    w8::commit_pair(&sh->empty[s]);
+                }
+                if (ok) w8::commit_pair(&sh->acc_full[b]);
+            }
+            // every MMA issued has retired before TMEM is freed (a wait that does not honour the abort flag: the operands
+            // are in place, so it ends)
+            w8::commit_one_of_pair(&sh->done);
+            tc::mbar_wait(&sh->done, 0, p.status, nullptr);
+        }
+    } else if (warp >= 4) {
+        const int e = warp - 4, q = warp & 3, half = e >> 2;
+        uint8_t* stage = out_stage + e * kStageOut;
+        uint32_t tl = 0;
+        int sbuf = 0;
+        bool ok = true;   // (a warp that gave up still meets the others at the barriers)
+        for (int t = first; t < g.tiles; t += step, tl++) {
+            const uint32_t b = tl & 1;
+            const int m0 = (t % g.tiles_m) * (2 * BM) + (int)rank * BM + 32 * q;
+            const int n0 = (t / g.tiles_m) * ROWS;
+            // channel scales of the tile: one a thread (256 epilogue threads, 256 columns)
+            w8::named_barrier(1, 32 * kEpiWarps);   // the last tile's are no longer read
+            {
+                const int c = threadIdx.x - 128;
+                const int n = n0 + (GATED ? c % BNC : c);
+                sh->sw[c] = n < p.n ? __ldg((GATED && c >= BNC ? p.scale_1 : p.scale_0) + n) : 0.0f;
+                if (!GATED) sh->bias[c] = p.bias && n < p.n ? __ldg(p.bias + n) : 0.0f;
+            }
+            w8::named_barrier(1, 32 * kEpiWarps);
+            const float sa = m0 + lane < p.m ? __ldg(p.scale_a + m0 + lane) : 0.0f;
+            ok = ok && tc::mbar_wait(&sh->acc_full[b], (tl >> 1) & 1, p.status, abort_flag);
+            if (!ok) continue;
+            tc::fence_after_sync();
+            const uint32_t tcol = tbase + ((uint32_t)(32 * q) << 16) + b * BN;
+            constexpr int CHUNKS = GATED ? 2 : 4;
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS; c++) {
+                const int col = half * (32 * CHUNKS) + 32 * c;   // the first of 32 output columns of the tile
+                uint32_t r[32], u[32];
+                tc::tmem_ld32(tcol + col, r);
+                if constexpr (GATED) tc::tmem_ld32(tcol + BNC + col, u);
+                w8::tmem_wait_ld32(r);
+                if constexpr (GATED) w8::tmem_wait_ld32(u);
+                if (c == CHUNKS - 1) {   // this warp's last read: the accumulator may be overwritten
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) w8::arrive_remote(w8::map_to_rank(&sh->acc_empty[b], 0));
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    float v = w8::rescale((int)r[j], sh->sw[col + j], sa);
+                    if constexpr (GATED) v = w8::gated(v, w8::rescale((int)u[j], sh->sw[BNC + col + j], sa), p.act);
+                    else if (p.bias) v = __fadd_rn(v, sh->bias[col + j]);
+                    r[j] = __float_as_uint(v);
+                }
+                // 32 x 32 values into this warp's staging rows (16-byte pieces in the TMA swizzle's places)
+                uint8_t* st = OUT32 ? stage : stage + 2048 * sbuf;
+                if (lane == 0) w8::bulk_wait_read<OUT32 ? 0 : 1>();   // the copy that last read this buffer
+                __syncwarp();
+                if constexpr (OUT32) {
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        *reinterpret_cast<uint4*>(st + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                            make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            o[j] = w8::bf16_pair(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
+                        *reinterpret_cast<uint4*>(st + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                const int nc = n0 + col;
+                if (nc >= p.n || m0 >= p.m) {   // (warp-uniform: nothing of this chunk is in y)
+                    __syncwarp();
+                    continue;
+                }
+                if (g.tma_out) {
+                    w8::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) w8::tma_store(&tm_y, st, nc, m0);
+                    if (lane == 0) w8::bulk_commit();
+                    sbuf ^= 1;
+                } else {
+                    __syncwarp();
+                    const int rows = min(32, p.m - m0);
+                    if (nc + lane < p.n)
+                        for (int i = 0; i < rows; i++) {
+                            const int64_t at = (int64_t)(m0 + i) * p.n + nc + lane;
+                            if (!q4_in_bounds(at, (int64_t)p.m * p.n, p.status)) continue;
+                            if constexpr (OUT32)
+                                static_cast<float*>(p.y)[at] =
+                                    *reinterpret_cast<const float*>(st + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + 4 * (lane & 3));
+                            else
+                                static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(
+                                    st + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + 2 * (lane & 7));
+                        }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) w8::bulk_wait_all();
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    w8::cluster_sync();       // no CTA leaves while its peer may still signal or read it
+    tc::fence_after_sync();
+    if (warp == 2) w8::tmem_dealloc_pair(tbase, 512);
+}
+
+}  // namespace
+
+int w8a8_gemm_launch(const Problem& p, cudaStream_t s)
+{
+    const bool gated = p.w1 != nullptr;
+    CUtensorMap mx, m0, m1, my;
+    if (!w8::make_code_map(&mx, p.xq, p.k, p.m, BM) || !w8::make_code_map(&m0, p.w0, p.k, p.n, BNC) ||
+        !w8::make_code_map(&m1, gated ? p.w1 : p.w0, p.k, p.n, BNC))
+        return Q4_ERR_CUDA;
+    Grid g;
+    g.tiles_m = (p.m + 2 * BM - 1) / (2 * BM);
+    const int rows = gated ? BNC : BN;
+    const int64_t tiles = (int64_t)g.tiles_m * ((p.n + rows - 1) / rows);
+    if (tiles > INT32_MAX) return Q4_ERR_SHAPE;
+    g.tiles = (int)tiles;
+    const int es = p.out_bf16 ? 2 : 4;
+    g.tma_out = ((int64_t)p.n * es) % 16 == 0;
+    if (g.tma_out) {
+        if (!w8::make_out_map(&my, p.y, p.n, p.m, p.out_bf16)) return Q4_ERR_CUDA;
+    } else {
+        my = mx;
+    }
+    const int pairs = (int)std::min<int64_t>(tiles, q4_num_sms() / 2);
+    auto go = [&](auto kern) {
+        if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return q4_cuda_status(e);
+        return q4_launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), kSmem, s, mx, m0, m1, my, p, g);
+    };
+    if (gated) return p.out_bf16 ? go(w8a8_gemm_kernel<true, false>) : go(w8a8_gemm_kernel<true, true>);
+    return p.out_bf16 ? go(w8a8_gemm_kernel<false, false>) : go(w8a8_gemm_kernel<false, true>);
+}
