@@ -24,12 +24,14 @@ using w8::Problem;
 constexpr int BM = 128;                 // token rows a CTA
 constexpr int BNC = 128;                // weight rows a CTA loads
 constexpr int BN = 2 * BNC;             // accumulator columns
-constexpr int BK = 128;                 // codes of K a stage
-constexpr int kStages = 5;
-constexpr int kStageBytes = (BM + BNC) * BK;
+constexpr int BK = 128;                 // codes of K a block (one swizzled 128-byte row)
+constexpr int kBlocks = 2;              // blocks a stage
+constexpr int kStages = 3;
+constexpr int kBlockBytes = (BM + BNC) * BK;
+constexpr int kStageBytes = kBlocks * kBlockBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kStageOut = 4096;         // output staging bytes an epilogue warp: 32 rows x (2 x 64 or 1 x 128) bytes
+constexpr int kStageOut = 4096;         // output staging bytes an epilogue warp: 32 rows x 128 bytes
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];   // full: the leader's (both CTAs' copies); empty: each CTA's
@@ -37,10 +39,10 @@ struct Shared {
     uint64_t done;
     uint32_t tmem;
     int abort_flag;
-    float sw[BN], bias[BN];                   // the tile's channel scales (gated: gate's, up's) and biases
+    alignas(16) float sw[BN], bias[BN];       // the tile's channel scales (gated: gate's, up's) and biases
 };
 
-constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + (int)sizeof(Shared);
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kStageOut + (int)sizeof(Shared);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Grid {
@@ -54,14 +56,17 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_y, const Problem p,
                  const Grid g)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];   // (whole 1024-byte swizzle atoms)
+    if (tc::smem_u32(smem) & 1023u) {                   // (never seen: the declared alignment is kept)
+        q4_set_status(p.status, Q4_ERR_ALIGN);
+        return;
+    }
     uint8_t* out_stage = smem + kStages * kStageBytes;
     Shared* sh = reinterpret_cast<Shared*>(out_stage + kEpiWarps * kStageOut);
     volatile int* abort_flag = &sh->abort_flag;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = w8::cluster_rank();
-    const int kblocks = (p.k + BK - 1) / BK;
+    const int kblocks = (p.k + BK - 1) / BK, kstages = (kblocks + kBlocks - 1) / kBlocks;
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
     constexpr int ROWS = GATED ? BNC : BN;   // weight rows (of each matrix) a tile covers
 
@@ -96,50 +101,64 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 const int m0 = (t % g.tiles_m) * (2 * BM) + (int)rank * BM;
                 const int n0 = (t / g.tiles_m) * ROWS + (GATED ? 0 : (int)rank * BNC);
                 const CUtensorMap* mw = GATED && rank ? &tm_w1 : &tm_w0;
-                for (int kb = 0; kb < kblocks; kb++, it++) {
+                for (int ks = 0; ks < kstages; ks++, it++) {
                     const int s = it % kStages;
                     if (!(ok = tc::mbar_wait(&sh->empty[s], ((it / kStages) & 1) ^ 1, p.status, abort_flag))) break;
-                    uint8_t* dst = smem + s * kStageBytes;
-                    if (rank == 0) tc::mbar_arrive_expect_tx(&sh->full[s], 2 * kStageBytes);
+                    const int nb = min(kBlocks, kblocks - ks * kBlocks);
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&sh->full[s], 2 * nb * kBlockBytes);
                     const uint32_t bar = w8::map_to_rank(&sh->full[s], 0);
-                    w8::tma_load_pair(dst, &tm_x, bar, kb * BK, m0);
-                    w8::tma_load_pair(dst + BM * BK, mw, bar, kb * BK, n0);
+                    for (int j = 0; j < nb; j++) {
+                        uint8_t* dst = smem + s * kStageBytes + j * kBlockBytes;
+                        w8::tma_load_pair(dst, &tm_x, bar, (ks * kBlocks + j) * BK, m0);
+                        w8::tma_load_pair(dst + BM * BK, mw, bar, (ks * kBlocks + j) * BK, n0);
+                    }
                 }
             }
             if (!ok) w8::pause_ns(100000000ull);   // given up: let the copies in flight land before the CTA leaves
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // The whole warp runs this loop and lane 0's predicate is on the instructions alone: measured 340 ns per four
+        // MMAs against 390 with the loop inside a branch of lane 0.  A barrier wait costs the issuer another ~130 ns (the
+        // MMAs before it drain), hence eight MMAs (two blocks of K) a wait.
+        if (rank == 0) {
             constexpr uint32_t idesc = w8::idesc_s8(2 * BM, BN);
             uint32_t it = 0, tl = 0;
             bool ok = true;
             for (int t = first; t < g.tiles && ok; t += step, tl++) {
                 const uint32_t b = tl & 1;
-                if (!(ok = tc::mbar_wait(&sh->acc_empty[b], ((tl >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+                if (!(ok = w8::warp_wait(&sh->acc_empty[b], ((tl >> 1) & 1) ^ 1, p.status, abort_flag))) break;
                 tc::fence_after_sync();
-                for (int kb = 0; kb < kblocks; kb++, it++) {
+                for (int ks = 0; ks < kstages; ks++, it++) {
                     const int s = it % kStages;
-                    if (!(ok = tc::mbar_wait(&sh->full[s], (it / kStages) & 1, p.status, abort_flag))) break;
+                    if (!(ok = w8::warp_wait(&sh->full[s], (it / kStages) & 1, p.status, abort_flag))) break;
                     tc::fence_after_sync();
-                    const uint32_t a = tc::smem_u32(smem + s * kStageBytes);
-                    const uint64_t ad = tc::smem_desc_sw128(a), bd = tc::smem_desc_sw128(a + BM * BK);
+                    const int nb = min(kBlocks, kblocks - ks * kBlocks);
 #pragma unroll
-                    for (int i = 0; i < BK / 32; i++)
-                        w8::mma_i8_pair(tbase + b * BN, ad + 2 * i, bd + 2 * i, idesc, kb > 0 || i > 0);
-                    w8::commit_pair(&sh->empty[s]);
+                    for (int j = 0; j < kBlocks; j++) {
+                        if (j >= nb) continue;
+                        const uint32_t a = tc::smem_u32(smem + s * kStageBytes + j * kBlockBytes);
+                        const uint64_t ad = tc::smem_desc_sw128(a), bd = tc::smem_desc_sw128(a + BM * BK);
+#pragma unroll
+                        for (int i = 0; i < BK / 32; i++)
+                            if (lane == 0) w8::mma_i8_pair(tbase + b * BN, ad + 2 * i, bd + 2 * i, idesc, ks > 0 || j > 0 || i > 0);
+                    }
+                    if (lane == 0) w8::commit_pair(&sh->empty[s]);
+                    __syncwarp();
                 }
-                if (ok) w8::commit_pair(&sh->acc_full[b]);
+                if (ok && lane == 0) w8::commit_pair(&sh->acc_full[b]);
+                __syncwarp();
             }
             // every MMA issued has retired before TMEM is freed (a wait that does not honour the abort flag: the operands
             // are in place, so it ends)
-            w8::commit_one_of_pair(&sh->done);
+            if (lane == 0) w8::commit_one_of_pair(&sh->done);
+            __syncwarp();
             tc::mbar_wait(&sh->done, 0, p.status, nullptr);
+            __syncwarp();
         }
     } else if (warp >= 4) {
         const int e = warp - 4, q = warp & 3, half = e >> 2;
         uint8_t* stage = out_stage + e * kStageOut;
         uint32_t tl = 0;
-        int sbuf = 0;
         bool ok = true;   // (a warp that gave up still meets the others at the barriers)
         for (int t = first; t < g.tiles; t += step, tl++) {
             const uint32_t b = tl & 1;
@@ -160,75 +179,87 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             tc::fence_after_sync();
             const uint32_t tcol = tbase + ((uint32_t)(32 * q) << 16) + b * BN;
             constexpr int CHUNKS = GATED ? 2 : 4;
+            constexpr int PER = OUT32 ? 1 : 2;                    // chunks a box: 128-byte rows
 #pragma unroll 1
-            for (int c = 0; c < CHUNKS; c++) {
-                const int col = half * (32 * CHUNKS) + 32 * c;   // the first of 32 output columns of the tile
-                uint32_t r[32], u[32];
-                tc::tmem_ld32(tcol + col, r);
-                if constexpr (GATED) tc::tmem_ld32(tcol + BNC + col, u);
-                w8::tmem_wait_ld32(r);
-                if constexpr (GATED) w8::tmem_wait_ld32(u);
-                if (c == CHUNKS - 1) {   // this warp's last read: the accumulator may be overwritten
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) w8::arrive_remote(w8::map_to_rank(&sh->acc_empty[b], 0));
-                }
+            for (int c0 = 0; c0 < CHUNKS; c0 += PER) {
 #pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    float v = w8::rescale((int)r[j], sh->sw[col + j], sa);
-                    if constexpr (GATED) v = w8::gated(v, w8::rescale((int)u[j], sh->sw[BNC + col + j], sa), p.act);
-                    else if (p.bias) v = __fadd_rn(v, sh->bias[col + j]);
-                    r[j] = __float_as_uint(v);
-                }
-                // 32 x 32 values into this warp's staging rows (16-byte pieces in the TMA swizzle's places)
-                uint8_t* st = OUT32 ? stage : stage + 2048 * sbuf;
-                if (lane == 0) w8::bulk_wait_read<OUT32 ? 0 : 1>();   // the copy that last read this buffer
-                __syncwarp();
-                if constexpr (OUT32) {
+                for (int c1 = 0; c1 < PER; c1++) {
+                    const int c = c0 + c1;
+                    const int col = half * (32 * CHUNKS) + 32 * c;   // the first of 32 output columns of the tile
+                    uint32_t r[32], u[32];
+                    tc::tmem_ld32(tcol + col, r);
+                    if constexpr (GATED) tc::tmem_ld32(tcol + BNC + col, u);
+                    w8::tmem_wait_ld32(r);
+                    if constexpr (GATED) w8::tmem_wait_ld32(u);
+                    if (c == CHUNKS - 1) {   // this warp's last read: the accumulator may be overwritten
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) w8::arrive_remote(w8::map_to_rank(&sh->acc_empty[b], 0));
+                    }
 #pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        *reinterpret_cast<uint4*>(st + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                            make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-                } else {
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 s0 = *reinterpret_cast<const float4*>(sh->sw + col + j);
+                        const float4 s1 = *reinterpret_cast<const float4*>(GATED ? sh->sw + BNC + col + j : sh->bias + col + j);
+                        const float f0[4] = {s0.x, s0.y, s0.z, s0.w}, f1[4] = {s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        uint32_t o[4];
+                        for (int i = 0; i < 4; i++) {
+                            float v = w8::rescale((int)r[j + i], f0[i], sa);
+                            if constexpr (GATED) v = w8::gated(v, w8::rescale((int)u[j + i], f1[i], sa), p.act);
+                            else if (p.bias) v = __fadd_rn(v, f1[i]);
+                            r[j + i] = __float_as_uint(v);
+                        }
+                    }
+                    // 32 rows into this warp's staging box (16-byte pieces in the TMA swizzle's places)
+                    if (c1 == 0) {
+                        if (lane == 0) w8::bulk_wait_read<0>();   // the copy that last read it
+                        __syncwarp();
+                    }
+                    if constexpr (OUT32) {
 #pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            o[j] = w8::bf16_pair(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
-                        *reinterpret_cast<uint4*>(st + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int k = 0; k < 8; k++)
+                            *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                o[j] = w8::bf16_pair(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
+                            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c1 + k) ^ (lane & 7)) << 4)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
+                        }
                     }
                 }
-                const int nc = n0 + col;
-                if (nc >= p.n || m0 >= p.m) {   // (warp-uniform: nothing of this chunk is in y)
-                    __syncwarp();
-                    continue;
-                }
-                if (g.tma_out) {
+                const int nc = n0 + half * (32 * CHUNKS) + 32 * c0;
+                constexpr int W = 32 * PER;             // columns of the box
+                const bool any = nc < p.n && m0 < p.m;   // (warp-uniform)
+                if (any && g.tma_out) {
                     w8::fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) w8::tma_store(&tm_y, st, nc, m0);
-                    if (lane == 0) w8::bulk_commit();
-                    sbuf ^= 1;
-                } else {
+                    if (lane == 0) {
+                        w8::tma_store(&tm_y, stage, nc, m0);
+                        w8::bulk_commit();
+                    }
+                } else if (any) {
                     __syncwarp();
                     const int rows = min(32, p.m - m0);
-                    if (nc + lane < p.n)
-                        for (int i = 0; i < rows; i++) {
-                            const int64_t at = (int64_t)(m0 + i) * p.n + nc + lane;
+                    for (int i = 0; i < rows; i++)
+                        for (int x = lane; x < W && nc + x < p.n; x += 32) {
+                            const int64_t at = (int64_t)(m0 + i) * p.n + nc + x;
                             if (!q4_in_bounds(at, (int64_t)p.m * p.n, p.status)) continue;
                             if constexpr (OUT32)
                                 static_cast<float*>(p.y)[at] =
-                                    *reinterpret_cast<const float*>(st + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + 4 * (lane & 3));
+                                    *reinterpret_cast<const float*>(stage + i * 128 + (((x >> 2) ^ (i & 7)) << 4) + 4 * (x & 3));
                             else
-                                static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(
-                                    st + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + 2 * (lane & 7));
+                                static_cast<uint16_t*>(p.y)[at] =
+                                    *reinterpret_cast<const uint16_t*>(stage + i * 128 + (((x >> 3) ^ (i & 7)) << 4) + 2 * (x & 7));
                         }
-                    __syncwarp();
                 }
+                __syncwarp();
             }
         }
-        if (lane == 0) w8::bulk_wait_all();
+        if (lane == 0) w8::bulk_wait_read<0>();   // (the grid's completion covers the writes)
     }
     tc::fence_before_sync();
     __syncwarp();

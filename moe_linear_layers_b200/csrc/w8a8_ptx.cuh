@@ -40,6 +40,12 @@ __device__ __forceinline__ void named_barrier(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// A whole warp's wait: every lane returns the same answer (a lane that gave up takes the others along).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag)
+{
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, abort_flag));
+}
+
 __device__ __forceinline__ void pause_ns(uint64_t ns)
 {
     const uint64_t t0 = tc::globaltimer_ns();
@@ -132,7 +138,6 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
@@ -162,10 +167,10 @@ inline bool make_code_map(CUtensorMap* map, const int8_t* base, int k, int rows,
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, k, rows, k, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// y [m][n], stored in boxes of 32 rows x 32 values; rows a multiple of 16 bytes
+// y [m][n], stored in boxes of 32 rows x 128 bytes; rows a multiple of 16 bytes
 inline bool make_out_map(CUtensorMap* map, void* y, int n, int m, bool bf16)
 {
-    return bf16 ? make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, n, m, 2 * (uint64_t)n, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)
+    return bf16 ? make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, n, m, 2 * (uint64_t)n, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B)
                 : make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, y, n, m, 4 * (uint64_t)n, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
