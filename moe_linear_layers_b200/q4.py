@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -114,7 +115,9 @@ _lib.moe_q4_forward_noalloc.argtypes = [_p, _i32, _i32, _p, _p, _i32, _i32, ctyp
                                         _i32, _p, _p, _p, _p, _p, _p, _p]
 _lib.q8_linear_w8a8.argtypes = [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p]
 _lib.q8_linear_w8a8_gated.argtypes = [_p, _p, _i32, _p, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p]
-_lib.block_norm.argtypes = [ctypes.POINTER(q4_block_norm), _i32, _i32, _p, _p]
+_lib.block_norm.argtypes = [_p, _i32, _i32, _p, _p]
+# a q4_block_norm from its fields in order, at a sixth of the cost of filling the ctypes structure
+_pack_block_norm = struct.Struct("9Q6i3f4x").pack
 
 
 class Q4Error(RuntimeError):
@@ -516,58 +519,82 @@ def q4_linear_w4a8(xq: torch.Tensor, scale_a: torch.Tensor, w: Q4Weight, out_dty
 # INT8 x INT8 products, their gated form, and the norms between blocks
 # ---------------------------------------------------------------------------------------------- #
 
-def _same(t, dtype, device, shape, name):
-    """A contiguous tensor of one dtype and shape on `device`."""
+def _same(t, dtype, dev, shape, name):
+    """The data pointer of a contiguous tensor of one dtype and shape on GPU `dev` (a decode step pays these checks
+    dozens of times, so the accepted case is one expression)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
-    return t.data_ptr()
+    if not t.is_cuda or t.get_device() != dev:
+        raise (ValueError if dev >= 0 else TypeError)(f"{name} is on {t.device}, the call's GPU is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _status(t, device):
-    """The caller's status word (nullable): an int32 tensor on the inputs' device."""
+def _status(t, dev):
+    """The caller's status word (nullable): an int32 tensor on the inputs' GPU."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.numel() < 1:
         raise TypeError("dev_status must be a torch.int32 tensor of one value")
-    if t.device != device:
-        raise ValueError(f"dev_status is on {t.device}, the inputs on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"dev_status is on {t.device}, the inputs on cuda:{dev}")
     return t.data_ptr()
 
 
-def _call(what, fn, args, device, stream, made, used):
-    """fn(*args, stream) on the inputs' device.  A call on a stream other than the device's current one marks the
-    tensors it was given and those it made as in use there (see _hold)."""
+def _call(what, fn, args, dev, stream, made, used):
+    """fn(*args, stream) on GPU `dev`.  A call on a stream other than the GPU's current one marks the tensors it was
+    given and those it made as in use there (see _hold)."""
     if stream is None:
-        if device.index == _current_device():
-            _check(fn(*args, _raw_current_stream(device.index)), what)
-            return
-        with torch.cuda.device(device):
-            _check(fn(*args, _raw_current_stream(device.index)), what)
-        return
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the inputs on {device}")
-    with torch.cuda.device(device):
-        _hold(stream, *made, *used)
-        _check(fn(*args, stream.cuda_stream), what)
+        if dev == _current_device():
+            rc = fn(*args, _raw_current_stream(dev))
+        else:
+            with torch.cuda.device(dev):
+                rc = fn(*args, _raw_current_stream(dev))
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the inputs on cuda:{dev}")
+        with torch.cuda.device(dev):
+            _hold(stream, *made, *used)
+            rc = fn(*args, stream.cuda_stream)
+    if rc:
+        _check(rc, what)
 
 
 def _w8_rows(xq, scale_a, wq, name):
-    """Check the codes of a W8A8 call: xq int8 [..][k] on a GPU, scale_a one per row, wq int8 [n][k].  Returns m, n, k."""
+    """The sizes and pointers of a W8A8 call's codes: xq int8 [..][k] on a GPU, scale_a one per row, wq int8 [n][k]."""
     if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
         raise ValueError(f"{name} must be an int8 tensor [n][k]")
-    _dev(xq, torch.int8, "xq")
+    if not isinstance(xq, torch.Tensor) or not xq.is_cuda:
+        raise TypeError("xq must be a CUDA tensor")
     n, k = wq.shape
-    if xq.dim() < 1 or xq.shape[-1] != k:
-        raise ValueError(f"xq has rows of {tuple(xq.shape)[-1:]}, {name} of {k} codes")
-    m = xq.numel() // k if k else 0
+    shape = xq.shape
+    if len(shape) < 1 or shape[-1] != k:
+        raise ValueError(f"xq has rows of {tuple(shape)[-1:]}, {name} of {k} codes")
+    m = shape[0] if len(shape) == 2 else xq.numel() // k if k else 0
+    dev = xq.get_device()
+    xp = _same(xq, torch.int8, dev, shape, "xq")
+    try:
+        if scale_a.dtype is torch.float32 and scale_a.numel() == m and scale_a.get_device() == dev and scale_a.is_contiguous():
+            return m, n, k, dev, xp, scale_a.data_ptr(), _same(wq, torch.int8, dev, (n, k), name)
+    except AttributeError:
+        pass
     _numel(_dev(scale_a, torch.float32, "scale_a"), m, "scale_a")
-    if scale_a.device != xq.device:
-        raise ValueError(f"scale_a is on {scale_a.device}, xq on {xq.device}")
-    return m, n, k
+    raise ValueError(f"scale_a is on {scale_a.device}, xq on {xq.device}")
+
+
+def _w8_out(y, m, n, out_dtype, xq, name):
+    """The output of a W8A8 call (made here unless the caller gives it) and its ABI code."""
+    if y is not None:
+        return y, _out(y, (m, n), xq.device, name)
+    if out_dtype is torch.bfloat16:
+        return torch.empty(m, n, dtype=torch.bfloat16, device=xq.device), Q4_OUT_BF16
+    if out_dtype is torch.float32:
+        return torch.empty(m, n, dtype=torch.float32, device=xq.device), Q4_OUT_F32
+    raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
 
 
 def q8_linear_w8a8(xq: torch.Tensor, scale_a: torch.Tensor, wq: torch.Tensor, scale_w: torch.Tensor,
@@ -576,15 +603,13 @@ def q8_linear_w8a8(xq: torch.Tensor, scale_a: torch.Tensor, wq: torch.Tensor, sc
     """y[m][n] = (xq[m][k] . wq[n][k]^T) * scale_w[n] * scale_a[m] (+ bias[n]) with an exact INT32 sum: INT8 codes and
     per-token scales as act_quant_per_token makes them, INT8 weights with one scale per output channel (the
     same call on the rows of a 16-bit weight makes those).  k % 16 == 0; fp32 or bf16 output."""
-    m, n, k = _w8_rows(xq, scale_a, wq, "wq")
-    dev = xq.device
-    if y is None:
-        y = torch.empty((m, n), dtype=out_dtype, device=dev)
-    args = (xq.data_ptr(), scale_a.data_ptr(), m, _same(wq, torch.int8, dev, (n, k), "wq"),
-            _same(scale_w, torch.float32, dev, (n,), "scale_w"), n, k,
-            None if bias is None else _same(bias, torch.float32, dev, (n,), "bias"), y.data_ptr(), _out(y, (m, n), dev),
-            _status(dev_status, dev))
-    _call("q8_linear_w8a8", _lib.q8_linear_w8a8, args, dev, stream, (y,), (xq, scale_a, wq, scale_w, bias, dev_status))
+    m, n, k, dev, xp, sp, wp = _w8_rows(xq, scale_a, wq, "wq")
+    y, od = _w8_out(y, m, n, out_dtype, xq, "y")
+    _call("q8_linear_w8a8", _lib.q8_linear_w8a8,
+          (xp, sp, m, wp, _same(scale_w, torch.float32, dev, (n,), "scale_w"), n, k,
+           None if bias is None else _same(bias, torch.float32, dev, (n,), "bias"), y.data_ptr(), od,
+           None if dev_status is None else _status(dev_status, dev)),
+          dev, stream, (y,), (xq, scale_a, wq, scale_w, bias, dev_status))
     return y
 
 
@@ -598,28 +623,25 @@ def q8_linear_w8a8_gated(xq: torch.Tensor, scale_a: torch.Tensor, wq_gate: torch
     one kernel.  act: "silu" or "gelu" (its tanh form)."""
     if act not in Q8_ACTS:
         raise ValueError(f"act must be one of {tuple(Q8_ACTS)}, got {act!r}")
-    m, n, k = _w8_rows(xq, scale_a, wq_gate, "wq_gate")
-    dev = xq.device
-    if h is None:
-        h = torch.empty((m, n), dtype=out_dtype, device=dev)
-    args = (xq.data_ptr(), scale_a.data_ptr(), m, _same(wq_gate, torch.int8, dev, (n, k), "wq_gate"),
-            _same(scale_gate, torch.float32, dev, (n,), "scale_gate"), _same(wq_up, torch.int8, dev, (n, k), "wq_up"),
-            _same(scale_up, torch.float32, dev, (n,), "scale_up"), n, k, Q8_ACTS[act], h.data_ptr(), _out(h, (m, n), dev, "h"),
-            _status(dev_status, dev))
-    _call("q8_linear_w8a8_gated", _lib.q8_linear_w8a8_gated, args, dev, stream, (h,),
-          (xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, dev_status))
+    m, n, k, dev, xp, sp, wp = _w8_rows(xq, scale_a, wq_gate, "wq_gate")
+    h, od = _w8_out(h, m, n, out_dtype, xq, "h")
+    _call("q8_linear_w8a8_gated", _lib.q8_linear_w8a8_gated,
+          (xp, sp, m, wp, _same(scale_gate, torch.float32, dev, (n,), "scale_gate"),
+           _same(wq_up, torch.int8, dev, (n, k), "wq_up"), _same(scale_up, torch.float32, dev, (n,), "scale_up"), n, k,
+           Q8_ACTS[act], h.data_ptr(), od, None if dev_status is None else _status(dev_status, dev)),
+          dev, stream, (h,), (xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, dev_status))
     return h
 
 
 _NORM_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-def _norm_rows(t, shape, device, name):
+def _norm_rows(t, shape, dev, name):
     """A contiguous fp32, bf16 or fp16 tensor of that shape; returns its pointer and dtype code."""
-    dt = _NORM_DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    dt = _NORM_DTYPES.get(getattr(t, "dtype", None))
     if dt is None:
         raise TypeError(f"{name} must be a torch.float32, torch.bfloat16 or torch.float16 CUDA tensor")
-    return _same(t, t.dtype, device, shape, name), dt
+    return _same(t, t.dtype, dev, shape, name), dt
 
 
 def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: torch.Tensor | None, post_w: torch.Tensor | None = None,
@@ -631,56 +653,66 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
     gate * branch_scale * b; n = norm(r) * pre_w.  x: the block's output [T][H] (None: only the residual is scaled
     and normed); residual [T][H] (None: r = the gated b); gate None, [H], or [G][H] (each row for T / G consecutive
     tokens).  Returns (r, n, xq, scale_a): r in the residual's dtype (x's without one; None unless want_residual), n in
-    out_dtype (None unless want_y), and with quant the INT8 codes and scales act_quant_per_token gives for n (else
+    out_dtype (None unless want_y), and with quant the INT8 codes of n and their per-token scales, amax / 127 (else
     None, None).  residual_out may be residual itself (in place).  fp32, bf16 or fp16 throughout; post_w and pre_w of
-    one dtype."""
+    one dtype.  Nothing here has a gradient."""
     lead = x if x is not None else residual
     if not isinstance(lead, torch.Tensor) or not lead.is_cuda or lead.dim() != 2:
         raise TypeError("x (or residual) must be a CUDA tensor [T][H]")
-    T, H = shape = lead.shape
-    dev = lead.device
-    if T == 0:
-        gate = None
-    d = q4_block_norm(eps=eps, res_scale=res_scale, branch_scale=branch_scale, gate_rows=1)
+    shape = lead.shape
+    T, H = shape
+    dev, device = lead.get_device(), lead.device
+    xp = rp = prep = postp = gp = rop = yp = qp = sp = 0
+    xd = rd = wd = gd = 0
+    gate_rows = 1
     if x is not None:
-        d.x, d.x_dtype = _norm_rows(x, shape, dev, "x")
+        xp, xd = _norm_rows(x, shape, dev, "x")
     if residual is not None:
-        d.residual, d.residual_dtype = _norm_rows(residual, shape, dev, "residual")
-    elif x is not None:
-        d.residual_dtype = d.x_dtype
+        rp, rd = _norm_rows(residual, shape, dev, "residual")
+        r_dtype = residual.dtype
+    else:
+        rd, r_dtype = xd, x.dtype
     if pre_w is not None:
-        d.pre_w, d.w_dtype = _norm_rows(pre_w, (H,), dev, "pre_w")
+        prep, wd = _norm_rows(pre_w, (H,), dev, "pre_w")
     if post_w is not None:
-        if pre_w is not None and pre_w.dtype != post_w.dtype:
+        if pre_w is not None and pre_w.dtype is not post_w.dtype:
             raise TypeError("post_w and pre_w must have the same dtype")
-        d.post_w, d.w_dtype = _norm_rows(post_w, (H,), dev, "post_w")
-    if gate is not None:
+        postp, wd = _norm_rows(post_w, (H,), dev, "post_w")
+    if gate is not None and T:
         if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2) or (gate.dim() == 2 and (gate.shape[0] < 1 or T % gate.shape[0])):
             raise ValueError(f"gate must be [H] or [G][H] with G a divisor of the {T} tokens")
-        d.gate, d.gate_dtype = _norm_rows(gate, (*gate.shape[:-1], H), dev, "gate")
-        d.gate_rows = gate.shape[0] if gate.dim() == 2 else 1
-    r_dtype = residual.dtype if residual is not None else x.dtype
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+        gp, gd = _norm_rows(gate, (gate_rows, H) if gate.dim() == 2 else (H,), dev, "gate")
     if want_residual:
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=r_dtype, device=dev)
-        d.residual_out = _same(residual_out, r_dtype, dev, shape, "residual_out")
+            residual_out = torch.empty(T, H, dtype=r_dtype, device=device)
+            rop = residual_out.data_ptr()
+        else:
+            rop = _same(residual_out, r_dtype, dev, shape, "residual_out")
     else:
         residual_out = None
-    d.y_dtype = _NORM_DTYPES.get(out_dtype if y is None or not want_y else y.dtype, -1)
-    if want_y:
-        if y is None:
-            y = torch.empty(shape, dtype=out_dtype, device=dev)
-        d.y, d.y_dtype = _norm_rows(y, shape, dev, "y")
+    if want_y and y is not None:
+        yp, yd = _norm_rows(y, shape, dev, "y")
     else:
-        y = None
+        yd = _NORM_DTYPES.get(out_dtype)
+        if yd is None:
+            raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
+        if want_y:
+            y = torch.empty(T, H, dtype=out_dtype, device=device)
+            yp = y.data_ptr()
+        else:
+            y = None
     if quant:
-        xq = torch.empty(shape, dtype=torch.int8, device=dev) if xq is None else xq
-        scale_a = torch.empty((T,), dtype=torch.float32, device=dev) if scale_a is None else scale_a
-        d.xq = _same(xq, torch.int8, dev, shape, "xq")
-        d.scale_a = _same(scale_a, torch.float32, dev, (T,), "scale_a")
+        if xq is None:
+            xq = torch.empty(T, H, dtype=torch.int8, device=device)
+        if scale_a is None:
+            scale_a = torch.empty(T, dtype=torch.float32, device=device)
+        qp = _same(xq, torch.int8, dev, shape, "xq")
+        sp = _same(scale_a, torch.float32, dev, (T,), "scale_a")
     else:
         xq = scale_a = None
-    _call("block_norm", _lib.block_norm, (ctypes.byref(d), T, H, _status(dev_status, dev)), dev, stream,
+    d = _pack_block_norm(xp, rp, postp, gp, prep, rop, yp, qp, sp, xd, rd, wd, gd, yd, gate_rows, eps, res_scale, branch_scale)
+    _call("block_norm", _lib.block_norm, (d, T, H, None if dev_status is None else _status(dev_status, dev)), dev, stream,
           (residual_out, y, xq, scale_a), (x, residual, post_w, gate, pre_w, dev_status))
     return residual_out, y, xq, scale_a
 
