@@ -14,7 +14,9 @@
 // orders of magnitude, so rstd does not depend on the order of the sum).  That pins n, and with it the
 // codes, which change by a whole step when a value crosses a rounding border.  The fp64 work is a conversion and a
 // multiply-add per value and norm, a few per cent of the fp64 pipe at the memory floor.
-#include "q4_common.cuh"
+#include <type_traits>
+
+#include "tc_ptx.cuh"
 
 namespace {
 
@@ -26,6 +28,8 @@ struct Args {
     int x_dt, r_dt, w_dt, g_dt, y_dt;
     int T, H, tokens_per_gate;
     float eps, res_scale, branch_scale;
+    double inv_h;
+    uint64_t ones;      // the fp32 pair (1, 1)
     int32_t* status;
 };
 
@@ -97,172 +101,688 @@ template <int V> __device__ __forceinline__ void store(void* p, int dt, int64_t 
 
 constexpr int kMaxWarps = 32;
 
-// sum over the CTA (every thread gets the same bits); `red` is free for reuse after the next barrier
-__device__ __forceinline__ double block_sum(double v, double* red)
+// What a CTA's reductions go through, twice: a fast warp may write the next row's while a slow one still reads
+struct Red {
+    double sum[2][2][kMaxWarps];
+    uint32_t top[2][kMaxWarps];
+};
+
+__device__ __forceinline__ double warp_sum(double v)
 {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
-    if (nw == 1) return v;
-    if (lane == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = lane < nw ? red[lane] : 0.0;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red)
+// sum over the CTA (WARP: over the warp); every thread gets the same bits
+template <bool WARP> __device__ __forceinline__ double row_sum(double v, double* red)
+{
+    v = warp_sum(v);
+    if constexpr (WARP) return v;
+    const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    return warp_sum(lane < nw ? red[lane] : 0.0);
+}
+
+template <bool WARP> __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red)
 {
     v = __reduce_max_sync(0xffffffffu, v);
+    if constexpr (WARP) return v;
     const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
-    if (nw == 1) return v;
     if (lane == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
     return __reduce_max_sync(0xffffffffu, lane < nw ? red[lane] : 0u);
 }
 
-// V values a load, P loads a thread: V * P * blockDim.x >= H
-template <int V, int P>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const Args a)
+template <int V> __device__ __forceinline__ void add_squares(const float (&v)[V], double& s)
 {
-    __shared__ double red[2][kMaxWarps];
-    __shared__ uint32_t redm[kMaxWarps];
-    q4_pdl_start();
-    const int64_t row = blockIdx.x, base = row * a.H;
-    const int nt = blockDim.x;
-    const double inv_h = 1.0 / a.H;
-    float v[P][V];
 #pragma unroll
-    for (int i = 0; i < P; i++) {
-        const int c = (i * nt + threadIdx.x) * V;
-#pragma unroll
-        for (int j = 0; j < V; j++) v[i][j] = 0.0f;
-        if (a.x && c < a.H) load<V>(a.x, a.x_dt, base + c, v[i]);
+    for (int j = 0; j < V; j++) s = fma((double)v[j], (double)v[j], s);
+}
+
+__device__ __forceinline__ float rstd_of(double sum, const Args& a)
+{
+    const double m = fma(sum, a.inv_h, (double)a.eps);
+    if (m > 1e-30 && m < 1e30) {
+        // the fp32 root (off by a relative d of 2^-22 or so) and one third-order step in fp64: off by d^3, and a
+        // fraction of the fp64 root's instructions, which every warp of a row would issue
+        const double r0 = (double)rsqrtf((float)m);
+        const double e = fma(-(m * r0), r0, 1.0);
+        return (float)fma(r0, fma(0.375, e, 0.5) * e, r0);
     }
-    if (a.x) {
-        if (a.post_w) {
-            double s = 0.0;
+    return (float)rsqrt(m);
+}
+
+template <int V> __device__ __forceinline__ void scale_by(float (&v)[V], float f)
+{
 #pragma unroll
-            for (int i = 0; i < P; i++)
+    for (int j = 0; j < V; j++) v[j] = __fmul_rn(v[j], f);
+}
+template <int V> __device__ __forceinline__ void scale_by(float (&v)[V], const float (&f)[V])
+{
 #pragma unroll
-                for (int j = 0; j < V; j++) s = fma((double)v[i][j], (double)v[i][j], s);
-            const float rs = (float)rsqrt(block_sum(s, red[0]) * inv_h + (double)a.eps);
+    for (int j = 0; j < V; j++) v[j] = __fmul_rn(v[j], f[j]);
+}
+
+// amax / 127, from the bits of amax, as a product with the fp32 reciprocal: an IEEE division would stand at the end of a
+// row's chain of reductions.  Off by at most 2^-23 of itself.
+__device__ __forceinline__ float scale_of(uint32_t top) { return __fmul_rn(__uint_as_float(top), 1.0f / 127.0f); }
+
+// v = what y_dt holds of v; the largest magnitude's bits (their order is the magnitudes', NaN on top)
+template <int V> __device__ __forceinline__ void settle(float (&v)[V], int dt, uint32_t& top)
+{
 #pragma unroll
-            for (int i = 0; i < P; i++) {
-                const int c = (i * nt + threadIdx.x) * V;
-                if (c >= a.H) continue;
-                float w[V];
-                load<V>(a.post_w, a.w_dt, c, w);
-#pragma unroll
-                for (int j = 0; j < V; j++) v[i][j] = __fmul_rn(__fmul_rn(v[i][j], rs), w[j]);
-            }
-        }
-        const int64_t grow = a.gate ? (row / a.tokens_per_gate) * a.H : 0;
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-            const int c = (i * nt + threadIdx.x) * V;
-            if (c >= a.H) continue;
-#pragma unroll
-            for (int j = 0; j < V; j++) v[i][j] = __fmul_rn(v[i][j], a.branch_scale);
-            if (a.gate) {
-                float g[V];
-                load<V>(a.gate, a.g_dt, grow + c, g);
-#pragma unroll
-                for (int j = 0; j < V; j++) v[i][j] = __fmul_rn(v[i][j], g[j]);
-            }
-        }
-    }
-    if (a.residual) {
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-            const int c = (i * nt + threadIdx.x) * V;
-            if (c >= a.H) continue;
-            float r[V];
-            load<V>(a.residual, a.r_dt, base + c, r);
-#pragma unroll
-            for (int j = 0; j < V; j++) {
-                r[j] = __fmul_rn(r[j], a.res_scale);
-                v[i][j] = a.x ? __fadd_rn(r[j], v[i][j]) : r[j];
-            }
-        }
-    }
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < P; i++)
-#pragma unroll
-        for (int j = 0; j < V; j++) s = fma((double)v[i][j], (double)v[i][j], s);
-    if (a.residual_out) {
-#pragma unroll
-        for (int i = 0; i < P; i++) {
-            const int c = (i * nt + threadIdx.x) * V;
-            if (c < a.H && q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status))
-                store<V>(a.residual_out, a.r_dt, base + c, v[i]);
-        }
-    }
-    if (!a.y && !a.xq) return;
-    const double ss = block_sum(s, red[1]);
-    const float rs = (float)rsqrt(ss * inv_h + (double)a.eps);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < P; i++) {
-        const int c = (i * nt + threadIdx.x) * V;
-        if (c >= a.H) continue;
-        float w[V];
-        if (a.pre_w) load<V>(a.pre_w, a.w_dt, c, w);
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-            v[i][j] = __fmul_rn(v[i][j], rs);
-            if (a.pre_w) v[i][j] = __fmul_rn(v[i][j], w[j]);
-        }
-        if (a.y && q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status)) store<V>(a.y, a.y_dt, base + c, v[i]);
-        if (a.xq) {
-#pragma unroll
-            for (int j = 0; j < V; j++) {
-                v[i][j] = as_stored(v[i][j], a.y_dt);
-                top = max(top, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);   // (bit order = magnitude order, NaN on top)
-            }
-        }
-    }
-    if (!a.xq) return;
-    top = block_max(top, redm);
-    const float scale = __uint_as_float(top) / 127.0f;
-    if (threadIdx.x == 0) {
-        a.scale_a[row] = scale;
-        if (top >= 0x7F800000u) q4_set_status(a.status, Q4_ERR_NONFINITE);
-    }
-    const bool exact_div = !(scale >= 0x1p-100f);
-    const float inv = exact_div ? 0.0f : 1.0f / scale;
-#pragma unroll
-    for (int i = 0; i < P; i++) {
-        const int c = (i * nt + threadIdx.x) * V;
-        if (c >= a.H) continue;
-        uint32_t o[V == 8 ? 2 : 1] = {};
-#pragma unroll
-        for (int j = 0; j < V; j++)
-            o[j / 4] |= (scale == 0.0f ? 0u : (uint32_t)q4_code8(v[i][j], scale, inv, exact_div) & 0xFFu) << (8 * (j & 3));
-        if (!q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status)) continue;
-        if constexpr (V == 8) *reinterpret_cast<uint2*>(a.xq + base + c) = make_uint2(o[0], o[1]);
-        else a.xq[base + c] = (int8_t)o[0];
+    for (int j = 0; j < V; j++) {
+        v[j] = as_stored(v[j], dt);
+        top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
 }
 
-template <int V> int launch(const Args& a, cudaStream_t s)
+// The codes of V values.  With a scale of at least 2^-100 the rounded quotient is at most 127 in magnitude (scale is amax /
+// 127 to 2^-23), so there is nothing to clamp and q + 1.5 * 2^23, rounded to nearest even like rint, holds the
+// code in its low byte.
+template <int V> __device__ __forceinline__ void store_codes(int8_t* p, const float (&v)[V], float scale, float inv, bool exact_div)
+{
+    uint32_t o[V == 8 ? 2 : 1] = {};
+    if (exact_div) {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            o[j / 4] |= (scale == 0.0f ? 0u : (uint32_t)q4_code8(v[j], scale, inv, true) & 0xFFu) << (8 * (j & 3));
+    } else {
+        uint32_t c[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            const float t = v[j] * inv;
+            c[j] = __float_as_uint(fmaf(fmaf(-scale, t, v[j]), inv, t) + 12582912.0f);
+        }
+        if constexpr (V == 2) {
+            o[0] = prmt(c[0], c[1], 0x0040u);
+        } else if constexpr (V == 8) {
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                o[h] = prmt(prmt(c[4 * h], c[4 * h + 1], 0x0040u), prmt(c[4 * h + 2], c[4 * h + 3], 0x0040u), 0x5410u);
+        } else {
+            o[0] = c[0];
+        }
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+    else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)o[0];
+    else *p = (int8_t)o[0];
+}
+
+// One row to a CTA of up to 1024 threads, or (WARP) to a warp of a CTA of 8: V values a load, P loads a thread.
+template <int V, int P, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Args a)
+{
+    __shared__ Red red;
+    q4_pdl_start();
+    const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
+    if (WARP && row >= a.T) return;
+    const int64_t base = row * a.H;
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    float v[P][V], r[P][V];
+    // both rows' loads go out before either is used
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int c = (i * nt + tid) * V;
+#pragma unroll
+        for (int j = 0; j < V; j++) v[i][j] = r[i][j] = 0.0f;
+        if (a.x && c < a.H) load<V>(a.x, a.x_dt, base + c, v[i]);
+        if (a.residual && c < a.H) load<V>(a.residual, a.r_dt, base + c, r[i]);
+    }
+    if (a.post_w) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < P; i++) add_squares<V>(v[i], s);
+        const float rs = rstd_of(row_sum<WARP>(s, red.sum[0][0]), a);
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+            const int c = (i * nt + tid) * V;
+            if (c >= a.H) continue;
+            float w[V];
+            load<V>(a.post_w, a.w_dt, c, w);
+            scale_by<V>(v[i], rs);
+            scale_by<V>(v[i], w);
+        }
+    }
+    const int64_t grow = a.gate ? (row / a.tokens_per_gate) * a.H : 0;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int c = (i * nt + tid) * V;
+        if (c >= a.H) continue;
+        if (a.x) scale_by<V>(v[i], a.branch_scale);
+        if (a.gate) {
+            float g[V];
+            load<V>(a.gate, a.g_dt, grow + c, g);
+            scale_by<V>(v[i], g);
+        }
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                r[i][j] = __fmul_rn(r[i][j], a.res_scale);
+                v[i][j] = a.x ? __fadd_rn(r[i][j], v[i][j]) : r[i][j];
+            }
+        }
+        add_squares<V>(v[i], s);
+        if (a.residual_out && q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status))
+            store<V>(a.residual_out, a.r_dt, base + c, v[i]);
+    }
+    if (!a.y && !a.xq) return;
+    const float rs = rstd_of(row_sum<WARP>(s, red.sum[0][1]), a);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int c = (i * nt + tid) * V;
+        if (c >= a.H) continue;
+        scale_by<V>(v[i], rs);
+        if (a.pre_w) {
+            float w[V];
+            load<V>(a.pre_w, a.w_dt, c, w);
+            scale_by<V>(v[i], w);
+        }
+        if (a.y && q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status)) store<V>(a.y, a.y_dt, base + c, v[i]);
+        if (a.xq) settle<V>(v[i], a.y_dt, top);
+    }
+    if (!a.xq) return;
+    top = row_max<WARP>(top, red.top[0]);
+    const float scale = scale_of(top);
+    if (tid == 0) {
+        a.scale_a[row] = scale;
+        if (top >= 0x7F800000u) q4_set_status(a.status, Q4_ERR_NONFINITE);
+    }
+    const bool exact_div = !(scale >= 0x1p-100f && scale < INFINITY);
+    const float inv = exact_div ? 0.0f : 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        const int c = (i * nt + tid) * V;
+        if (c < a.H && q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status))
+            store_codes<V>(a.xq + base + c, v[i], scale, inv, exact_div);
+    }
+}
+
+// Many rows: one persistent CTA of 16 warps an SM.  A team of W warps (1 up to 1024 values a row) owns a row at a time, E
+// values a lane in registers, so a row's two sums and its maximum cost a lane a few instructions for E values
+// and, with one warp a team, no barrier.  (With 256 threads a row the reductions alone were a fifth of 78 instructions a
+// value: 2.1 TB/s.)  Rows come ahead of use by bulk copies into the team's ring in shared memory: x, the residual, and
+// the gate's row where it changes with the token.  A copy covers the 16-byte pieces that hold the row, so rows of any width
+// and alignment take this path: V values are then read at a time (8, 2, 1), where the row allows.  What every row
+// shares (the norms' weights, a single gate) is kept as fp32 in shared memory.
+struct Ring {
+    int stages, warps, teams;        // slots a team, warps a team, teams a CTA
+    int slot[3];                     // bytes of a slot's x, residual and gate pieces (0: not in the ring)
+    int post, gate, pre;             // where the shared vectors start (bytes; -1: none)
+    int rings;                       // where the rings start
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)   // max(a, |b|), NaN wins
+{
+    float d;
+    asm("{\n\t.reg .f32 m;\n\tabs.f32 m, %2;\n\tmax.NaN.f32 %0, %1, m;\n\t}" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return tc::f2_pack(__float_as_uint(lo), __float_as_uint(hi)); }
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 64 values a lane need 128 registers, fewer fit in 100
+__host__ __device__ constexpr int team_threads(int e) { return e == 64 ? 512 : 640; }
+constexpr int kMaxSlots = 48;   // stages x teams
+
+// V values of type DT at p
+template <int V, int DT> __device__ __forceinline__ void get(const uint8_t* p, float (&v)[V])
+{
+    if constexpr (V == 8) {
+        load<8>(p, DT, 0, v);
+    } else if constexpr (V == 2) {
+        if constexpr (DT == Q4_F32) {
+            const float2 a = *reinterpret_cast<const float2*>(p);
+            v[0] = a.x;
+            v[1] = a.y;
+        } else {
+            const uint32_t e = *reinterpret_cast<const uint32_t*>(p);
+            if constexpr (DT == Q4_BF16) {
+                v[0] = __uint_as_float(e << 16);
+                v[1] = __uint_as_float(e & 0xFFFF0000u);
+            } else {
+                const float2 f = __half22float2(u32_as_h2(e));
+                v[0] = f.x;
+                v[1] = f.y;
+            }
+        }
+    } else {
+        load<1>(p, DT, 0, v);
+    }
+}
+
+template <int V, int DT> __device__ __forceinline__ void put(uint8_t* p, const float (&v)[V])
+{
+    if constexpr (V == 2) {
+        if constexpr (DT == Q4_F32) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+        else if constexpr (DT == Q4_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+            *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(&h);
+        } else *reinterpret_cast<uint32_t*>(p) = h2_as_u32(__floats2half2_rn(v[0], v[1]));
+    } else {
+        store<V>(p, DT, 0, v);
+    }
+}
+
+// f(DT) for the type dt: one branch around a whole row's work instead of one per value
+template <typename F> __device__ __forceinline__ void by_type(int dt, F f)
+{
+    if (dt == Q4_BF16) f(std::integral_constant<int, Q4_BF16>());
+    else if (dt == Q4_F32) f(std::integral_constant<int, Q4_F32>());
+    else f(std::integral_constant<int, Q4_F16>());
+}
+
+// A shared vector in fp32: V == 8 keeps the two halves of each 8 values apart, so that a warp's 16-byte reads of
+// consecutive pieces touch every bank once.
+template <int V> __device__ __forceinline__ int shared_at(int c, int j, int H)
+{
+    return V == 8 ? (j >> 2) * (H / 2) + (c >> 1) + (j & 3) : c + j;
+}
+
+template <int V, int E, bool FULL>
+__global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(const Args a, const Ring q)
+{
+    constexpr int C = E / V, kTeamThreads = team_threads(E);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kMaxSlots];
+    __shared__ double red_sum[2][2][kTeamThreads / 32];
+    __shared__ float red_top[2][kTeamThreads / 32];
+    __shared__ volatile int abort_flag;   // one lane's wait ran out: the others' end too
+    const int H = a.H, W = q.warps, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int team = warp / W, first_warp = team * W, tl = (warp - first_warp) * 32 + lane, tt = 32 * W;
+    const int slot_bytes = q.slot[0] + q.slot[1] + q.slot[2];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < q.stages * q.teams; i++) tc::mbar_init(&full[i], 1);
+        abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    q4_pdl_start();
+    const bool live = team < q.teams;
+    const int64_t step = (int64_t)gridDim.x * q.teams, row0 = (int64_t)blockIdx.x * q.teams + team;
+    uint8_t* ring = smem + q.rings + (int64_t)team * q.stages * slot_bytes;
+    const int xs = a.x_dt == Q4_F32 ? 4 : 2, rs_ = a.r_dt == Q4_F32 ? 4 : 2, gs = a.g_dt == Q4_F32 ? 4 : 2;
+    const int64_t g_rows = q.slot[2] ? a.T / a.tokens_per_gate : 0;
+
+    // the 16-byte pieces of row i of an array of n rows; the array's last bytes past a whole piece are left out (tail)
+    auto piece = [&](const void* base, int64_t i, int64_t n, int es, const uint8_t*& src, uint32_t& bytes) {
+        const int64_t b0 = i * H * es & ~(int64_t)15, end = n * H * es & ~(int64_t)15;
+        const int64_t b1 = ((i + 1) * H * es + 15) & ~(int64_t)15;
+        src = static_cast<const uint8_t*>(base) + b0;
+        bytes = (uint32_t)((b1 < end ? b1 : end) - b0);
+    };
+    auto fetch = [&](int64_t row, int s) {   // one lane
+        uint8_t* dst = ring + (int64_t)s * slot_bytes;
+        uint64_t* bar = &full[team * q.stages + s];
+        const uint8_t *px = nullptr, *pr = nullptr, *pg = nullptr;
+        uint32_t bx = 0, br = 0, bg = 0;
+        if (q.slot[0]) piece(a.x, row, a.T, xs, px, bx);
+        if (q.slot[1]) piece(a.residual, row, a.T, rs_, pr, br);
+        if (q.slot[2]) piece(a.gate, row / a.tokens_per_gate, g_rows, gs, pg, bg);
+        tc::mbar_arrive_expect_tx(bar, bx + br + bg);
+        if (bx) bulk_load(dst, px, bx, bar);
+        if (br) bulk_load(dst + q.slot[0], pr, br, bar);
+        if (bg) bulk_load(dst + q.slot[0] + q.slot[1], pg, bg, bar);
+    };
+    if (live && tl == 0)
+        for (int i = 0; i < q.stages; i++)
+            if (row0 + i * step < a.T) fetch(row0 + i * step, i);
+    // the shared vectors into shared memory, the three vectors' loads side by side
+    for (int c = threadIdx.x * V; c < H; c += kTeamThreads * V) {
+        float w[3][V];
+        auto read = [&](const void* p, int dt, bool on, float (&f)[V]) {
+            if (on) by_type(dt, [&](auto DT) { get<V, DT()>(static_cast<const uint8_t*>(p) + (int64_t)c * (DT() == Q4_F32 ? 4 : 2), f); });
+        };
+        auto keep = [&](int at, const float (&f)[V]) {
+            if (at >= 0)
+#pragma unroll
+                for (int j = 0; j < V; j++) reinterpret_cast<float*>(smem + at)[shared_at<V>(c, j, H)] = f[j];
+        };
+        read(a.post_w, a.w_dt, q.post >= 0, w[0]);
+        read(a.gate, a.g_dt, q.gate >= 0, w[1]);
+        read(a.pre_w, a.w_dt, q.pre >= 0, w[2]);
+        keep(q.post, w[0]);
+        keep(q.gate, w[1]);
+        keep(q.pre, w[2]);
+    }
+    __syncthreads();
+    if (!live) return;
+    const float* s_post = reinterpret_cast<const float*>(smem + (q.post < 0 ? 0 : q.post));
+    const float* s_gate = reinterpret_cast<const float*>(smem + (q.gate < 0 ? 0 : q.gate));
+    const float* s_pre = reinterpret_cast<const float*>(smem + (q.pre < 0 ? 0 : q.pre));
+
+    auto team_sync = [&] {
+        if (W == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(tt) : "memory");
+    };
+    auto team_sum = [&](double v, double* red) {
+        v = warp_sum(v);
+        if (W == 1) return v;
+        if (lane == 0) red[warp] = v;
+        team_sync();
+        v = red[first_warp];
+        for (int i = 1; i < W; i++) v += red[first_warp + i];
+        return v;
+    };
+
+    // A warp owns E * 32 consecutive values of the row, a lane V of each 32 V: chunk i is at a constant offset from the
+    // lane's first value c0, and in the row while i * 32 V < left.
+    const int c0 = (warp - first_warp) * (32 * E) + lane * V, left = H - c0;
+    constexpr int D = 32 * V;   // between a lane's chunks
+    // the first row of each array whose end lies behind the array's last whole piece
+    auto first_cut = [&](int64_t n, int es) { return (n * H * es & ~(int64_t)15) / ((int64_t)H * es); };
+    const int64_t cut[3] = {q.slot[0] ? first_cut(a.T, xs) : a.T, q.slot[1] ? first_cut(a.T, rs_) : a.T, first_cut(g_rows, gs)};
+    int s = -1, par = 1;
+    uint32_t phase = 1;
+    bool ok = true;   // (a thread that gives up still meets its team; the row is then undefined)
+    for (int64_t row = row0; row < a.T; row += step) {
+        par ^= 1;
+        if (++s == q.stages) s = 0;
+        if (s == 0) phase ^= 1;
+        const int64_t base = row * H;
+        uint8_t* src = ring + (int64_t)s * slot_bytes;
+        ok = ok && tc::mbar_wait(&full[team * q.stages + s], phase, a.status, &abort_flag);
+        if (V != 8 && (row >= cut[0] || row >= cut[1] || (q.slot[2] && row / a.tokens_per_gate >= cut[2]))) {
+            // the bytes past an array's last whole piece (the end of its last row, for short rows of several)
+            auto tail = [&](const void* p, int64_t i, int64_t n, int es, uint8_t* dst) {
+                const int64_t b0 = i * H * es & ~(int64_t)15, end = n * H * es & ~(int64_t)15;
+                const int64_t hi = (i + 1) * H * es;
+                for (int64_t b = (end > b0 ? end : b0) + 2 * tl; b < hi; b += 2 * tt)
+                    *reinterpret_cast<uint16_t*>(dst + (b - b0)) = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(p) + b);
+            };
+            if (q.slot[0]) tail(a.x, row, a.T, xs, src);
+            if (q.slot[1]) tail(a.residual, row, a.T, rs_, src + q.slot[0]);
+            if (q.slot[2]) tail(a.gate, row / a.tokens_per_gate, g_rows, gs, src + q.slot[0] + q.slot[1]);
+            team_sync();
+        }
+        // the lane's E values in pairs, for the packed fp32 instructions (each half rounds like the scalar one); a
+        // chunk's V values are consecutive, and what is not of the row stays 0
+        uint64_t v[E / 2];
+#pragma unroll
+        for (int i = 0; i < E / 2; i++) v[i] = q.slot[0] ? 0 : 0x8000000080000000ull;
+        // each: f(chunk) for this lane's chunks of the row
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < C; i++)
+                if (FULL || i * D < left) f(i);
+        };
+        auto all = [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < E / 2; i++) v[i] = f(v[i]);
+        };
+        auto times = [&](float f) {
+            const uint64_t f2 = pair(f, f);
+            all([&](uint64_t x) { return f2_mul(x, f2); });
+        };
+        // values of type DT at p (chunk i at p + i * D values) combined with v pair by pair: v = f(v, value)
+        auto with = [&](const uint8_t* p, auto DT, auto f) {
+            constexpr int es = DT() == Q4_F32 ? 4 : 2;
+            if constexpr (V == 1) {
+#pragma unroll
+                for (int i = 0; i < C; i += 2) {
+                    float lo[1] = {0.0f}, hi[1] = {0.0f};
+                    if (i * D < left) get<1, DT()>(p + i * (D * es), lo);
+                    if ((i + 1) * D < left) get<1, DT()>(p + (i + 1) * (D * es), hi);
+                    v[i / 2] = f(v[i / 2], pair(lo[0], hi[0]));
+                }
+            } else {
+                each([&](int i) {
+                    float w[V];
+                    get<V, DT()>(p + i * (D * es), w);
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) v[(i * V + j) / 2] = f(v[(i * V + j) / 2], pair(w[j], w[j + 1]));
+                });
+            }
+        };
+        auto times_shared = [&](const float* sm) {
+            if constexpr (V == 8) {
+                const float* p0 = sm + (c0 >> 1);
+                const float* p1 = p0 + H / 2;
+                each([&](int i) {
+                    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(p0 + i * (D / 2));
+                    const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(p1 + i * (D / 2));
+                    v[4 * i] = f2_mul(v[4 * i], lo.x);
+                    v[4 * i + 1] = f2_mul(v[4 * i + 1], lo.y);
+                    v[4 * i + 2] = f2_mul(v[4 * i + 2], hi.x);
+                    v[4 * i + 3] = f2_mul(v[4 * i + 3], hi.y);
+                });
+            } else {
+                with(reinterpret_cast<const uint8_t*>(sm + c0), std::integral_constant<int, Q4_F32>(), f2_mul);
+            }
+        };
+        auto squares = [&] {   // four chains: one would wait for each multiply-add
+            double s4[4] = {};
+#pragma unroll
+            for (int i = 0; i < E / 2; i++) {
+                const double lo = (double)tc::f2_lo(v[i]), hi = (double)tc::f2_hi(v[i]);
+                s4[2 * (i & 1)] = fma(lo, lo, s4[2 * (i & 1)]);
+                s4[2 * (i & 1) + 1] = fma(hi, hi, s4[2 * (i & 1) + 1]);
+            }
+            return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        };
+        if (q.slot[0]) {
+            by_type(a.x_dt, [&](auto DT) {
+                constexpr int es = DT() == Q4_F32 ? 4 : 2;
+                with(src + (base * es & 15) + c0 * es, DT, [](uint64_t, uint64_t x) { return x; });
+            });
+            if (a.post_w) {
+                times(rstd_of(team_sum(squares(), red_sum[par][0]), a));
+                times_shared(s_post);
+            }
+            if (a.branch_scale != 1.0f) times(a.branch_scale);
+            if (q.slot[2])
+                by_type(a.g_dt, [&](auto DT) {
+                    constexpr int es = DT() == Q4_F32 ? 4 : 2;
+                    with(src + q.slot[0] + q.slot[1] + (row / a.tokens_per_gate * H * es & 15) + c0 * es, DT, f2_mul);
+                });
+            else if (q.gate >= 0) times_shared(s_gate);
+        }
+        if (q.slot[1]) {
+            // The sum is a multiply-add by a one the compiler does not know: a packed product that feeds a packed sum was
+            // seen to be contracted with it into one rounding (mul.rn.f32x2, add.rn.f32x2, CUDA 12.9), which moves r' by
+            // more than an ulp where the residual and the branch cancel.  (Without x the sum is with -0, which leaves every
+            // value, -0 among them, as it is.)
+            const uint64_t rs2 = pair(a.res_scale, a.res_scale);
+            by_type(a.r_dt, [&](auto DT) {
+                constexpr int es = DT() == Q4_F32 ? 4 : 2;
+                with(src + q.slot[0] + (base * es & 15) + c0 * es, DT,
+                     [&](uint64_t x, uint64_t r) { return tc::f2_fma(f2_mul(r, rs2), a.ones, x); });
+            });
+        }
+        const float rs = rstd_of(team_sum(squares(), red_sum[par][1]), a);
+        // every lane of the team has read the slot (the sum's barrier, or the warp's shuffles, lie behind the reads)
+        {
+            __syncwarp();
+            const int64_t next = row + q.stages * step;
+            if (tl == 0 && ok && next < a.T) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                fetch(next, s);
+            }
+        }
+        auto chunk = [&](int i, float (&w)[V]) {
+#pragma unroll
+            for (int j = 0; j < V; j++) w[j] = (i * V + j) & 1 ? tc::f2_hi(v[(i * V + j) / 2]) : tc::f2_lo(v[(i * V + j) / 2]);
+        };
+        auto write = [&](void* out, auto DT) {
+            constexpr int es = DT() == Q4_F32 ? 4 : 2;
+            uint8_t* p = static_cast<uint8_t*>(out) + (base + c0) * es;
+            each([&](int i) {
+                float w[V];
+                chunk(i, w);
+                if (q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) put<V, DT()>(p + i * (D * es), w);
+            });
+        };
+        if (a.residual_out) by_type(a.r_dt, [&](auto DT) { write(a.residual_out, DT); });
+        if (!a.y && !a.xq) continue;
+        times(rs);
+        if (q.pre >= 0) times_shared(s_pre);
+        float top = 0.0f;
+        by_type(a.y_dt, [&](auto DT) {
+            if (a.y) write(a.y, DT);
+            if (a.xq)
+                all([&](uint64_t x) {
+                    float lo = tc::f2_lo(x), hi = tc::f2_hi(x);
+                    if constexpr (DT() == Q4_BF16) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                        const uint32_t e = *reinterpret_cast<const uint32_t*>(&h);
+                        lo = __uint_as_float(e << 16);
+                        hi = __uint_as_float(e & 0xFFFF0000u);
+                    } else {
+                        lo = as_stored(lo, DT());
+                        hi = as_stored(hi, DT());
+                    }
+                    top = max_nan(max_nan(top, lo), hi);
+                    return pair(lo, hi);
+                });
+        });
+        if (!a.xq) continue;
+        uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // (bit order = order of magnitudes, NaN on top)
+        if (W > 1) {
+            if (lane == 0) red_top[par][warp] = __uint_as_float(tb);
+            team_sync();
+            for (int i = 0; i < W; i++) tb = max(tb, __float_as_uint(red_top[par][first_warp + i]));
+        }
+        const float scale = scale_of(tb);
+        if (tl == 0) {
+            a.scale_a[row] = scale;
+            if (tb >= 0x7F800000u) q4_set_status(a.status, Q4_ERR_NONFINITE);
+        }
+        const bool exact_div = !(scale >= 0x1p-100f && scale < INFINITY);
+        int8_t* out = a.xq + base + c0;
+        if (exact_div) {
+            each([&](int i) {
+                float w[V];
+                chunk(i, w);
+                if (q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) store_codes<V>(out + i * D, w, scale, 0.0f, true);
+            });
+        } else {
+            // the quotient and the rounding of store_codes, two values at a time
+            const float inv = 1.0f / scale;
+            const uint64_t inv2 = pair(inv, inv), neg2 = pair(-scale, -scale), magic = pair(12582912.0f, 12582912.0f);
+            all([&](uint64_t x) {
+                const uint64_t t = f2_mul(x, inv2);
+                return tc::f2_add(tc::f2_fma(tc::f2_fma(neg2, t, x), inv2, t), magic);
+            });
+            each([&](int i) {
+                if (!q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) return;
+                auto bytes = [&](int j) { return prmt((uint32_t)v[j], (uint32_t)(v[j] >> 32), 0x0040u); };   // a pair's codes
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint2*>(out + i * D) = make_uint2(prmt(bytes(4 * i), bytes(4 * i + 1), 0x5410u),
+                                                                        prmt(bytes(4 * i + 2), bytes(4 * i + 3), 0x5410u));
+                else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(out + i * D) = (uint16_t)bytes(i);
+                else out[i * D] = (int8_t)(i & 1 ? v[i / 2] >> 32 : v[i / 2]);
+            });
+        }
+    }
+    if (!ok && tl == 0) {   // given up: no copy may land in the memory of the CTA that follows
+        const uint64_t t0 = tc::globaltimer_ns();
+        for (uint32_t i = 0; !tc::wait_expired(t0, 100000000ull, i, 64); i++) __nanosleep(1000);
+    }
+}
+
+template <int V> int launch_rows(const Args& a, cudaStream_t s)
 {
     const int words = (a.H + V - 1) / V;
+    // a warp a row while that leaves a lane at most 32 values (no barrier; a CTA for each would hold few rows an SM)
+    if (words <= 32 * (32 / V)) {
+        const dim3 grid((unsigned)((a.T + (int64_t)7) / 8)), block(256);
+        if (words <= 32) return q4_launch_pdl(block_norm_kernel<V, 1, true>, grid, block, 0, s, a);
+        if (words <= 64) return q4_launch_pdl(block_norm_kernel<V, 2, true>, grid, block, 0, s, a);
+        if constexpr (V == 8) return q4_launch_pdl(block_norm_kernel<V, 4, true>, grid, block, 0, s, a);
+        else if (words <= 256) return q4_launch_pdl(block_norm_kernel<V, 8, true>, grid, block, 0, s, a);
+    }
     const int p = (words + 1023) / 1024;
     const dim3 grid(a.T), block(p > 1 ? 1024 : (words + 31) / 32 * 32);
-    if (p <= 1) return q4_launch_pdl(block_norm_kernel<V, 1>, grid, block, 0, s, a);
-    if (p <= 2) return q4_launch_pdl(block_norm_kernel<V, 2>, grid, block, 0, s, a);
-    if (p <= 4) return q4_launch_pdl(block_norm_kernel<V, 4>, grid, block, 0, s, a);
+    if (p <= 1) return q4_launch_pdl(block_norm_kernel<V, 1, false>, grid, block, 0, s, a);
+    if (p <= 2) return q4_launch_pdl(block_norm_kernel<V, 2, false>, grid, block, 0, s, a);
+    if (p <= 4) return q4_launch_pdl(block_norm_kernel<V, 4, false>, grid, block, 0, s, a);
     if constexpr (V == 1) {
-        if (p <= 16) return q4_launch_pdl(block_norm_kernel<V, 16>, grid, block, 0, s, a);
-        return q4_launch_pdl(block_norm_kernel<V, 32>, grid, block, 0, s, a);
+        if (p <= 16) return q4_launch_pdl(block_norm_kernel<V, 16, false>, grid, block, 0, s, a);
+        return q4_launch_pdl(block_norm_kernel<V, 32, false>, grid, block, 0, s, a);
     }
     return Q4_ERR_SHAPE;
 }
 
-int64_t dtype_size(int dt) { return dt == Q4_F32 ? 4 : 2; }
+int elem_bytes(int dt) { return dt == Q4_F32 ? 4 : 2; }
+
+// The persistent form for E values a lane: Q4_ERR_UNSUPPORTED where the shape does not suit it
+int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream_t s)
+{
+    const int sms = q4_num_sms();
+    const int V = a.H % 8 == 0 ? 8 : a.H % 2 == 0 ? 2 : 1;
+    Ring q = {};
+    q.warps = (a.H + 32 * E - 1) / (32 * E);
+    if (q.warps > team_threads(E) / 32) return Q4_ERR_UNSUPPORTED;
+    const bool full = V == 8 && a.H == 32 * E * q.warps;
+    auto slot = [&](bool on, int dt) { return on ? (a.H * elem_bytes(dt) + 15) / 16 * 16 + (V == 8 ? 0 : 16) : 0; };
+    q.slot[0] = slot(a.x, a.x_dt);
+    q.slot[1] = slot(a.residual, a.r_dt);
+    q.slot[2] = slot(many_gates, a.g_dt);
+    const int row = q.slot[0] + q.slot[1] + q.slot[2];
+    int at = 0;
+    auto vec = [&](bool on) {
+        const int here = at;
+        if (!on) return -1;
+        at += (4 * a.H + 15) / 16 * 16;
+        return here;
+    };
+    q.post = vec(a.post_w);
+    q.gate = vec(a.gate && !many_gates);
+    q.pre = vec(a.pre_w);
+    q.rings = at;
+    const int room = 224 * 1024 - at;
+    q.teams = std::min(team_threads(E) / 32 / q.warps, room / row);
+    if (q.teams < 1 || a.T < (int64_t)min_rows * sms * q.teams) return Q4_ERR_UNSUPPORTED;
+    q.stages = std::min({3, room / (row * q.teams), kMaxSlots / q.teams});
+    const int smem = at + q.stages * q.teams * row;
+    auto go = [&](auto kern) {
+        if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return q4_cuda_status(e);
+        return q4_launch_pdl(kern, dim3(sms), dim3(team_threads(E)), smem, s, a, q);
+    };
+    if (full) return E == 64 ? go(block_norm_team_kernel<8, 64, true>) : E == 32 ? go(block_norm_team_kernel<8, 32, true>)
+                                                                                 : go(block_norm_team_kernel<8, 16, true>);
+    if (V == 8) return E == 64 ? go(block_norm_team_kernel<8, 64, false>) : E == 32 ? go(block_norm_team_kernel<8, 32, false>)
+                                                                                    : go(block_norm_team_kernel<8, 16, false>);
+    if (E == 64) return Q4_ERR_UNSUPPORTED;   // (spills)
+    if (V == 2) return E == 32 ? go(block_norm_team_kernel<2, 32, false>) : go(block_norm_team_kernel<2, 16, false>);
+    return E == 32 ? go(block_norm_team_kernel<1, 32, false>) : go(block_norm_team_kernel<1, 16, false>);
+}
+
+// When there are rows enough for the persistent form, measured against a CTA or a warp a row (us, bf16, every part):
+//   H 256: 12000 rows 16.7 / 10.5 (a warp a row has no ring to fill: never)     H 512: 1200 rows 5.3 / 6.3
+//   H 1000: 600 rows 8.2 / 10.3     H 1001: 600 rows 11.8 / 11.9, 4800 rows 22.6 / 74.8
+//   H 2048: 1200 rows 11.3 / 10.7, 4800 rows 25.0 / 29.7     H 8192: 300 rows 12.9 / 15.9, 4800 rows 70 / 165
+// The most values a lane that leave each team two rows and the lanes four fifths full come first (long rows of few lanes
+// cost the fewest instructions); with fewer rows, more warps share one.
+int launch_many(const Args& a, bool many_gates, cudaStream_t s)
+{
+    if (a.H <= 256) return Q4_ERR_UNSUPPORTED;
+    int rc = Q4_ERR_UNSUPPORTED;
+    for (int E = 64; E >= 16 && rc == Q4_ERR_UNSUPPORTED; E /= 2) {
+        const int cap = (a.H + 32 * E - 1) / (32 * E) * 32 * E;
+        if (5 * a.H >= 4 * cap || E == 16) rc = launch_teams(a, E, 2, many_gates, s);
+    }
+    if (rc != Q4_ERR_UNSUPPORTED) return rc;
+    if (a.H <= 1024 || a.H % 8) return a.T >= 4 * q4_num_sms() ? launch_teams(a, a.H <= 512 ? 16 : 32, 0, many_gates, s) : rc;
+    return a.H > 4096 ? launch_teams(a, 16, 1, many_gates, s) : rc;
+}
 
 // two arrays share memory (NULL shares none)
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
@@ -298,10 +818,10 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
     // an output may replace the input of the same rows and element size, and overlap nothing else
     const int64_t n = (int64_t)T * H;
     const void* in[5] = {d->x, d->residual, d->post_w, d->pre_w, d->gate};
-    const int64_t in_n[5] = {n * dtype_size(d->x_dtype), n * dtype_size(d->residual_dtype), H * dtype_size(d->w_dtype),
-                             H * dtype_size(d->w_dtype), (int64_t)d->gate_rows * H * dtype_size(d->gate_dtype)};
+    const int64_t in_n[5] = {n * (int64_t)elem_bytes(d->x_dtype), n * (int64_t)elem_bytes(d->residual_dtype), H * (int64_t)elem_bytes(d->w_dtype),
+                             H * (int64_t)elem_bytes(d->w_dtype), (int64_t)d->gate_rows * H * (int64_t)elem_bytes(d->gate_dtype)};
     const void* out[4] = {d->residual_out, d->y, d->xq, d->scale_a};
-    const int64_t out_n[4] = {n * dtype_size(d->residual_dtype), n * dtype_size(d->y_dtype), n, 4 * (int64_t)T};
+    const int64_t out_n[4] = {n * (int64_t)elem_bytes(d->residual_dtype), n * (int64_t)elem_bytes(d->y_dtype), n, 4 * (int64_t)T};
     for (int o = 0; o < 4; o++) {
         for (int i = 0; i < 5; i++) {
             const bool in_place = o < 2 && i < 2 && out[o] == in[i] && out_n[o] == in_n[i];
@@ -331,10 +851,17 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
     a.eps = d->eps;
     a.res_scale = d->res_scale;
     a.branch_scale = d->branch_scale;
+    a.inv_h = 1.0 / H;
+    a.ones = 0x3F8000003F800000ull;
     a.status = dev_status;
-    // 16-byte accesses need rows and arrays that start on 16 bytes (8 for the codes); otherwise one value at a time
-    const bool vec = H % 8 == 0 && q4_aligned16(d->x) && q4_aligned16(d->residual) && q4_aligned16(d->residual_out) &&
-                     q4_aligned16(d->post_w) && q4_aligned16(d->pre_w) && q4_aligned16(d->gate) && q4_aligned16(d->y) &&
-                     ((uintptr_t)d->xq & 7u) == 0;
-    return vec ? launch<8>(a, (cudaStream_t)stream) : launch<1>(a, (cudaStream_t)stream);
+    // Arrays that start on 16 bytes (8 for the codes) take the persistent form when there are rows enough, and
+    // 16-byte accesses when H % 8 == 0 keeps the rows so; anything else goes one value at a time.
+    const bool whole = q4_aligned16(d->x) && q4_aligned16(d->residual) && q4_aligned16(d->residual_out) &&
+                       q4_aligned16(d->post_w) && q4_aligned16(d->pre_w) && q4_aligned16(d->gate) && q4_aligned16(d->y) &&
+                       ((uintptr_t)d->xq & 7u) == 0;
+    if (whole) {
+        const int rc = launch_many(a, d->gate && d->gate_rows > 1, (cudaStream_t)stream);
+        if (rc != Q4_ERR_UNSUPPORTED) return rc;
+    }
+    return whole && H % 8 == 0 ? launch_rows<8>(a, (cudaStream_t)stream) : launch_rows<1>(a, (cudaStream_t)stream);
 }
