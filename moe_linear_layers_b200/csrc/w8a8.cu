@@ -15,9 +15,49 @@ PFN_cuTensorMapEncodeTiled_v12000 w8::tensor_map_encoder()
 }
 
 int w8a8_gemm_launch(const w8::Problem& p, cudaStream_t s);
+int w8a8_split_launch(const w8::Problem& p, int bn, int splits, cudaStream_t s);
 int w8a8_small_launch(const w8::Problem& p, cudaStream_t s);
 
 namespace {
+
+// Which kernel: the streaming one for few tokens, else the faster of the split and the pair kernel by their times.
+//
+// Streaming: its tokens come in groups of 16 that each read the weights again.  It is the faster one up to 8 tokens, and
+// beyond while the groups read about 24 MB in all (us, streaming / split: 2048 x 2048, 64 tokens 4.7 / 5.5; 8192 x 2048, 17 tokens
+// 6.7 / 6.9, 32 tokens 7.9 / 6.8; gated 8192 x 2048, 16 tokens 12.0 / 9.5).
+//
+// The other two by what was measured on B200 (16 and 64 blocks of K, 8 to 1024 tokens), in us:
+//   split: 3.3 + bn / (36 splits) + bn / 128 for the exchange + 0.24 to 0.43 a block of K, for each wave of CTAs
+//   pair:  4.7 + 0.27 a block of K a wave, and 3 more from the second wave on
+// (2048 x 8192, 65 tokens: split 9.2, pair 22.4; 2048 x 2048, 512 tokens: 9.2 / 9.9; 8192 x 2048, 256 tokens: 13.3 / 10.5.)
+struct Choice {
+    int bn, splits;   // bn 0: the pair kernel
+};
+
+Choice choose(const w8::Problem& p)
+{
+    const bool gated = p.w1 != nullptr;
+    const int kb = (p.k + 127) / 128, sms = q4_num_sms();
+    auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t pair_waves = ceil_div(ceil_div(p.m, 256) * ceil_div(p.n, gated ? 128 : 256), sms / 2);
+    double best = 4.7 + 0.27 * kb * pair_waves + 3.0 * (pair_waves - 1);
+    Choice c = {0, 1};
+    const int64_t tiles_n = ceil_div(p.n, gated ? 64 : 128);
+    for (int i = 0; i < 4; i++) {
+        const int bn = 32 << i;
+        const double block[4] = {0.24, 0.26, 0.36, 0.43};
+        if (i > 0 && bn >= 2 * p.m) break;   // (a narrower tile holds every token)
+        for (int splits = 1; splits <= 4 && splits <= kb; splits *= 2) {
+            const int64_t waves = ceil_div(tiles_n * ceil_div(p.m, bn) * splits, sms);
+            const double t = 1.5 + waves * (1.8 + bn / (36.0 * splits) + (splits > 1 ? bn / 128.0 : 0.0) + block[i] * ceil_div(kb, splits));
+            if (t < best) {
+                best = t;
+                c = {bn, splits};
+            }
+        }
+    }
+    return c;
+}
 
 int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
 {
@@ -28,7 +68,10 @@ int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
     if (!q4_aligned16(p.xq) || !q4_aligned16(p.w0) || !q4_aligned16(p.w1) || !q4_aligned16(p.y) ||
         (((uintptr_t)p.scale_a | (uintptr_t)p.scale_0 | (uintptr_t)p.scale_1 | (uintptr_t)p.bias) & 3u))
         return Q4_ERR_ALIGN;
-    return p.m <= 64 ? w8a8_small_launch(p, s) : w8a8_gemm_launch(p, s);
+    const int64_t groups = (p.m + 15) / 16;
+    if (p.m <= 8 || (p.m <= 64 && groups * p.n * p.k * (p.w1 ? 2 : 1) <= (24 << 20))) return w8a8_small_launch(p, s);
+    const Choice c = choose(p);
+    return c.bn ? w8a8_split_launch(p, c.bn, c.splits, s) : w8a8_gemm_launch(p, s);
 }
 
 }  // namespace

@@ -243,18 +243,21 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     }
                 } else if (any) {
                     __syncwarp();
+                    // rows that do not start on 16 bytes: a warp stores 32 columns of a row at a time
+                    constexpr int ES = OUT32 ? 4 : 2;
                     const int rows = min(32, p.m - m0);
-                    for (int i = 0; i < rows; i++)
-                        for (int x = lane; x < W && nc + x < p.n; x += 32) {
-                            const int64_t at = (int64_t)(m0 + i) * p.n + nc + x;
-                            if (!q4_in_bounds(at, (int64_t)p.m * p.n, p.status)) continue;
-                            if constexpr (OUT32)
-                                static_cast<float*>(p.y)[at] =
-                                    *reinterpret_cast<const float*>(stage + i * 128 + (((x >> 2) ^ (i & 7)) << 4) + 4 * (x & 3));
-                            else
-                                static_cast<uint16_t*>(p.y)[at] =
-                                    *reinterpret_cast<const uint16_t*>(stage + i * 128 + (((x >> 3) ^ (i & 7)) << 4) + 2 * (x & 7));
+                    for (int x = lane; x < W; x += 32) {
+                        if (nc + x >= p.n) continue;
+                        const int piece = x * ES >> 4, inner = x * ES & 15;
+                        uint8_t* dst = static_cast<uint8_t*>(p.y) + ((int64_t)m0 * p.n + nc + x) * ES;
+#pragma unroll 8
+                        for (int i = 0; i < rows; i++, dst += (int64_t)p.n * ES) {
+                            const uint8_t* src = stage + i * 128 + ((piece ^ (i & 7)) << 4) + inner;
+                            if (!q4_in_bounds((int64_t)(m0 + i) * p.n + nc + x, (int64_t)p.m * p.n, p.status)) continue;
+                            if constexpr (OUT32) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+                            else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
                         }
+                    }
                 }
                 __syncwarp();
             }

@@ -6,15 +6,14 @@
 // k slots are given the bytes that a 16-byte load brings: lane (g, t) takes bytes 16 t .. 16 t + 15 of each 64-byte
 // block of rows g and g + 8 (weights) and of token g (activations), and the four words fill two MMAs' slots.
 //
-// Memory-bound: n * k bytes of weights.  The CTA's 8 warps split k in 128-byte blocks, and
-// meet once through shared memory.
+// Memory-bound: n * k bytes of weights.  The CTA's warps split k in 128-byte blocks, and meet
+// once through shared memory.
 #include "w8a8_common.cuh"
 
 namespace {
 
 using w8::Problem;
 
-constexpr int kWarps = 8;
 constexpr int kRows = 16;
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -29,10 +28,11 @@ __device__ __forceinline__ uint4 ld16(const int8_t* p, bool ok)
     return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// MT: groups of 8 tokens a CTA; MATS: 1, or 2 = gate and up
-template <int MT, int MATS>
+// MT: groups of 8 tokens a CTA; MATS: 1, or 2 = gate and up; U: blocks of k whose loads are in flight together
+template <int MT, int MATS, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32) w8a8_small_kernel(const Problem p)
 {
+    constexpr int U = MT * MATS == 1 ? 4 : 2;
     __shared__ int part[kWarps][MATS * kRows * 8 * MT];
     q4_pdl_start();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32) w8a8_small_kernel(const Problem p
         xok[i] = m0 + 8 * i + g < p.m;
         xr[i] = p.xq + (int64_t)(xok[i] ? m0 + 8 * i + g : 0) * p.k;
     }
-#pragma unroll 2
+#pragma unroll U
     for (int k0 = warp * 128; k0 < p.k; k0 += kWarps * 128) {
         uint4 w[2][MATS][2], x[2][MT];
 #pragma unroll
@@ -106,12 +106,16 @@ __global__ void __launch_bounds__(kWarps * 32) w8a8_small_kernel(const Problem p
     }
 }
 
+// 8 warps a CTA, or 16 where 8 would leave an SM fewer than 16 and k gives each of the 16 a block or more (2048 rows, k 8192,
+// one token: 6.2 us with 8 warps)
 template <int MT> int launch(const Problem& p, cudaStream_t s)
 {
     const dim3 grid((p.n + kRows - 1) / kRows, (p.m + 8 * MT - 1) / (8 * MT));
     if (grid.y > 65535) return Q4_ERR_SHAPE;
-    return p.w1 ? q4_launch_pdl(w8a8_small_kernel<MT, 2>, grid, dim3(kWarps * 32), 0, s, p)
-                : q4_launch_pdl(w8a8_small_kernel<MT, 1>, grid, dim3(kWarps * 32), 0, s, p);
+    const bool more = (int64_t)grid.x * grid.y <= q4_num_sms() && p.k >= 16 * 128;
+    auto go = [&](auto kern, int warps) { return q4_launch_pdl(kern, grid, dim3(32 * warps), 0, s, p); };
+    if (p.w1) return more ? go(w8a8_small_kernel<MT, 2, 16>, 16) : go(w8a8_small_kernel<MT, 2, 8>, 8);
+    return more ? go(w8a8_small_kernel<MT, 1, 16>, 16) : go(w8a8_small_kernel<MT, 1, 8>, 8);
 }
 
 }  // namespace
