@@ -545,44 +545,39 @@ def _status(t, dev):
     return t.data_ptr()
 
 
-def _call(what, fn, args, dev, stream, made, used):
-    """fn(*args, stream) on GPU `dev`.  A call on a stream other than the GPU's current one marks the tensors it was
-    given and those it made as in use there (see _hold)."""
-    if stream is None:
-        if dev == _current_device():
-            rc = fn(*args, _raw_current_stream(dev))
-        else:
-            with torch.cuda.device(dev):
-                rc = fn(*args, _raw_current_stream(dev))
-    else:
-        if stream.device.index != dev:
-            raise ValueError(f"the stream is on {stream.device}, the inputs on cuda:{dev}")
-        with torch.cuda.device(dev):
-            _hold(stream, *made, *used)
-            rc = fn(*args, stream.cuda_stream)
-    if rc:
-        _check(rc, what)
+def _elsewhere(what, fn, args, dev, stream, tensors):
+    """fn(*args, stream) on GPU `dev` where that is not the current device, or on a stream that is not its current one:
+    the call's tensors, its own and the caller's, are then marked in use there (see _hold)."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the inputs on cuda:{dev}")
+    with torch.cuda.device(dev):
+        _hold(stream, *tensors)
+        _check(fn(*args, _raw_current_stream(dev) if stream is None else stream.cuda_stream), what)
 
 
 def _w8_rows(xq, scale_a, wq, name):
     """The sizes and pointers of a W8A8 call's codes: xq int8 [..][k] on a GPU, scale_a one per row, wq int8 [n][k]."""
+    try:
+        n, k = wq.shape
+        shape = xq.shape
+        dev = xq.get_device()
+        m = shape[0] if len(shape) == 2 else xq.numel() // k
+        if (dev >= 0 and shape[-1] == k and xq.dtype is torch.int8 and xq.is_contiguous()
+                and scale_a.dtype is torch.float32 and scale_a.numel() == m and scale_a.get_device() == dev and scale_a.is_contiguous()
+                and wq.dtype is torch.int8 and wq.get_device() == dev and wq.is_contiguous()):
+            return m, n, k, dev, xq.data_ptr(), scale_a.data_ptr(), wq.data_ptr()
+    except (AttributeError, ValueError, IndexError, ZeroDivisionError):
+        pass
+    # what is wrong
     if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
         raise ValueError(f"{name} must be an int8 tensor [n][k]")
     if not isinstance(xq, torch.Tensor) or not xq.is_cuda:
         raise TypeError("xq must be a CUDA tensor")
-    n, k = wq.shape
-    shape = xq.shape
-    if len(shape) < 1 or shape[-1] != k:
-        raise ValueError(f"xq has rows of {tuple(shape)[-1:]}, {name} of {k} codes")
-    m = shape[0] if len(shape) == 2 else xq.numel() // k if k else 0
-    dev = xq.get_device()
-    xp = _same(xq, torch.int8, dev, shape, "xq")
-    try:
-        if scale_a.dtype is torch.float32 and scale_a.numel() == m and scale_a.get_device() == dev and scale_a.is_contiguous():
-            return m, n, k, dev, xp, scale_a.data_ptr(), _same(wq, torch.int8, dev, (n, k), name)
-    except AttributeError:
-        pass
-    _numel(_dev(scale_a, torch.float32, "scale_a"), m, "scale_a")
+    if xq.dim() < 1 or xq.shape[-1] != wq.shape[1] or wq.shape[1] == 0:
+        raise ValueError(f"xq has rows of {tuple(xq.shape)[-1:]}, {name} of {wq.shape[1]} codes")
+    _dev(xq, torch.int8, "xq")
+    _same(wq, torch.int8, xq.get_device(), wq.shape, name)
+    _numel(_dev(scale_a, torch.float32, "scale_a"), xq.numel() // wq.shape[1], "scale_a")
     raise ValueError(f"scale_a is on {scale_a.device}, xq on {xq.device}")
 
 
@@ -605,11 +600,16 @@ def q8_linear_w8a8(xq: torch.Tensor, scale_a: torch.Tensor, wq: torch.Tensor, sc
     same call on the rows of a 16-bit weight makes those).  k % 16 == 0; fp32 or bf16 output."""
     m, n, k, dev, xp, sp, wp = _w8_rows(xq, scale_a, wq, "wq")
     y, od = _w8_out(y, m, n, out_dtype, xq, "y")
-    _call("q8_linear_w8a8", _lib.q8_linear_w8a8,
-          (xp, sp, m, wp, _same(scale_w, torch.float32, dev, (n,), "scale_w"), n, k,
-           None if bias is None else _same(bias, torch.float32, dev, (n,), "bias"), y.data_ptr(), od,
-           None if dev_status is None else _status(dev_status, dev)),
-          dev, stream, (y,), (xq, scale_a, wq, scale_w, bias, dev_status))
+    swp = _same(scale_w, torch.float32, dev, (n,), "scale_w")
+    bp = None if bias is None else _same(bias, torch.float32, dev, (n,), "bias")
+    st = None if dev_status is None else _status(dev_status, dev)
+    if stream is None and dev == _current_device():
+        rc = _lib.q8_linear_w8a8(xp, sp, m, wp, swp, n, k, bp, y.data_ptr(), od, st, _raw_current_stream(dev))
+        if rc:
+            _check(rc, "q8_linear_w8a8")
+    else:
+        _elsewhere("q8_linear_w8a8", _lib.q8_linear_w8a8, (xp, sp, m, wp, swp, n, k, bp, y.data_ptr(), od, st), dev, stream,
+                   (y, xq, scale_a, wq, scale_w, bias, dev_status))
     return y
 
 
@@ -625,11 +625,17 @@ def q8_linear_w8a8_gated(xq: torch.Tensor, scale_a: torch.Tensor, wq_gate: torch
         raise ValueError(f"act must be one of {tuple(Q8_ACTS)}, got {act!r}")
     m, n, k, dev, xp, sp, wp = _w8_rows(xq, scale_a, wq_gate, "wq_gate")
     h, od = _w8_out(h, m, n, out_dtype, xq, "h")
-    _call("q8_linear_w8a8_gated", _lib.q8_linear_w8a8_gated,
-          (xp, sp, m, wp, _same(scale_gate, torch.float32, dev, (n,), "scale_gate"),
-           _same(wq_up, torch.int8, dev, (n, k), "wq_up"), _same(scale_up, torch.float32, dev, (n,), "scale_up"), n, k,
-           Q8_ACTS[act], h.data_ptr(), od, None if dev_status is None else _status(dev_status, dev)),
-          dev, stream, (h,), (xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, dev_status))
+    sgp = _same(scale_gate, torch.float32, dev, (n,), "scale_gate")
+    up, sup = _same(wq_up, torch.int8, dev, (n, k), "wq_up"), _same(scale_up, torch.float32, dev, (n,), "scale_up")
+    st = None if dev_status is None else _status(dev_status, dev)
+    if stream is None and dev == _current_device():
+        rc = _lib.q8_linear_w8a8_gated(xp, sp, m, wp, sgp, up, sup, n, k, Q8_ACTS[act], h.data_ptr(), od, st, _raw_current_stream(dev))
+        if rc:
+            _check(rc, "q8_linear_w8a8_gated")
+    else:
+        _elsewhere("q8_linear_w8a8_gated", _lib.q8_linear_w8a8_gated,
+                   (xp, sp, m, wp, sgp, up, sup, n, k, Q8_ACTS[act], h.data_ptr(), od, st), dev, stream,
+                   (h, xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, dev_status))
     return h
 
 
@@ -638,9 +644,12 @@ _NORM_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 def _norm_rows(t, shape, dev, name):
     """A contiguous fp32, bf16 or fp16 tensor of that shape; returns its pointer and dtype code."""
-    dt = _NORM_DTYPES.get(getattr(t, "dtype", None))
-    if dt is None:
-        raise TypeError(f"{name} must be a torch.float32, torch.bfloat16 or torch.float16 CUDA tensor")
+    try:
+        dt = _NORM_DTYPES[t.dtype]
+        if t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), dt
+    except (AttributeError, KeyError):
+        raise TypeError(f"{name} must be a torch.float32, torch.bfloat16 or torch.float16 CUDA tensor") from None
     return _same(t, t.dtype, dev, shape, name), dt
 
 
@@ -705,15 +714,25 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
     if quant:
         if xq is None:
             xq = torch.empty(T, H, dtype=torch.int8, device=device)
+            qp = xq.data_ptr()
+        else:
+            qp = _same(xq, torch.int8, dev, shape, "xq")
         if scale_a is None:
             scale_a = torch.empty(T, dtype=torch.float32, device=device)
-        qp = _same(xq, torch.int8, dev, shape, "xq")
-        sp = _same(scale_a, torch.float32, dev, (T,), "scale_a")
+            sp = scale_a.data_ptr()
+        else:
+            sp = _same(scale_a, torch.float32, dev, (T,), "scale_a")
     else:
         xq = scale_a = None
     d = _pack_block_norm(xp, rp, postp, gp, prep, rop, yp, qp, sp, xd, rd, wd, gd, yd, gate_rows, eps, res_scale, branch_scale)
-    _call("block_norm", _lib.block_norm, (d, T, H, None if dev_status is None else _status(dev_status, dev)), dev, stream,
-          (residual_out, y, xq, scale_a), (x, residual, post_w, gate, pre_w, dev_status))
+    st = None if dev_status is None else _status(dev_status, dev)
+    if stream is None and dev == _current_device():
+        rc = _lib.block_norm(d, T, H, st, _raw_current_stream(dev))
+        if rc:
+            _check(rc, "block_norm")
+    else:
+        _elsewhere("block_norm", _lib.block_norm, (d, T, H, st), dev, stream,
+                   (residual_out, y, xq, scale_a, x, residual, post_w, gate, pre_w, dev_status))
     return residual_out, y, xq, scale_a
 
 
