@@ -1,16 +1,21 @@
 // Entry points of the INT8 x INT8 (W8A8) products: argument checks and the choice of kernel by size.
+#include <atomic>
+
 #include "w8a8_common.cuh"
 #include "w8a8_ptx.cuh"
 
 PFN_cuTensorMapEncodeTiled_v12000 w8::tensor_map_encoder()
 {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> kept{nullptr};   // (a failed look-up is tried again)
+    PFN_cuTensorMapEncodeTiled_v12000 fn = kept.load(std::memory_order_relaxed);
+    if (!fn) {
         cudaDriverEntryPointQueryResult q;
         void* f = nullptr;
-        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-                        q == cudaDriverEntryPointSuccess;
-        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
-    }();
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess) {
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+            kept.store(fn, std::memory_order_relaxed);
+        }
+    }
     return fn;
 }
 
@@ -46,7 +51,7 @@ Choice choose(const w8::Problem& p)
     for (int i = 0; i < 4; i++) {
         const int bn = 32 << i;
         const double block[4] = {0.24, 0.26, 0.36, 0.43};
-        if (i > 0 && bn >= 2 * p.m) break;   // (a narrower tile holds every token)
+        if (i > 0 && bn / 2 >= p.m) break;   // (a narrower tile holds every token)
         for (int splits = 1; splits <= 4 && splits <= kb; splits *= 2) {
             const int64_t waves = ceil_div(tiles_n * ceil_div(p.m, bn) * splits, sms);
             const double t = 1.5 + waves * (1.8 + bn / (36.0 * splits) + (splits > 1 ? bn / 128.0 : 0.0) + block[i] * ceil_div(kb, splits));
@@ -61,7 +66,7 @@ Choice choose(const w8::Problem& p)
 
 int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
 {
-    if (p.m < 0 || p.n < 0 || p.k < 16 || p.k > Q8_MAX_K || p.k % 16) return Q4_ERR_SHAPE;
+    if (p.m < 0 || p.n < 0 || p.m > Q8_MAX_ROWS || p.n > Q8_MAX_ROWS || p.k < 16 || p.k > Q8_MAX_K || p.k % 16) return Q4_ERR_SHAPE;
     if (out_dtype != Q4_OUT_F32 && out_dtype != Q4_OUT_BF16) return Q4_ERR_UNSUPPORTED;
     if (p.m == 0 || p.n == 0) return Q4_OK;   // an empty product reads and writes nothing
     if (!p.xq || !p.scale_a || !p.w0 || !p.scale_0 || !p.y || (p.w1 && !p.scale_1)) return Q4_ERR_NULL;

@@ -34,6 +34,7 @@ Q4_ERR_BOUNDS = -9
 Q4_OUT_F32 = 0
 Q4_OUT_BF16 = 1
 Q8_MAX_K = 131056
+Q8_MAX_ROWS = 1 << 30
 Q4_BLOCK_NORM_MAX_H = 32768
 
 EXPORTED = ("q4_status_string", "q4_version", "q4_build_flags", "q4_last_cuda_error_string", "q4_quantize_pack", "q4_linear_w4a16", "q4_linear_w4a16_max_gemv_m",

@@ -176,6 +176,20 @@ def test_in_place_and_single_outputs(q4, T, H):
     assert out is res and yy is x and torch.equal(res, r) and torch.equal(x, y) and torch.equal(q, xq) and torch.equal(s, sa)
 
 
+def test_rows_past_32_bits(q4):
+    """More than 2^31 values: the last rows are where they belong."""
+    T, H = 270000, 8192
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    some = torch.randn((5, H), device="cuda", generator=g)
+    x = torch.zeros((T, H), dtype=BF16, device="cuda")
+    x[-5:] = some.to(BF16)
+    _, y, xq, sa = q4.block_norm(x, None, None, quant=True, want_residual=False)
+    _, y5, xq5, sa5 = q4.block_norm(x[-5:].clone(), None, None, quant=True, want_residual=False)
+    assert torch.equal(y[-5:], y5) and torch.equal(xq[-5:], xq5) and torch.equal(sa[-5:], sa5)
+    assert not bool(y[: T - 5].any()) and not bool(sa[: T - 5].any())
+
+
 def test_offset_views(q4):
     """Rows that start off 16 bytes, and the memory around the outputs."""
     T, H = 19, 64

@@ -67,7 +67,7 @@ SHAPES = [
     (9, 128, 128), (16, 2048, 8192), (17, 255, 272), (31, 64, 4096), (33, 1003, 1040), (64, 512, 512), (77, 129, 144),
     (100, 2048, 2048), (128, 128, 16), (129, 257, 112), (200, 1024, 2048), (255, 8192, 512), (256, 256, 256),
     (333, 1003, 1040), (512, 2048, 2048), (513, 40, 8192), (1000, 8, 2048), (1025, 1025, 1024), (2048, 512, 2048),
-    (2049, 4100, 528),
+    (2049, 4100, 528), (3, 128256, 256), (300, 70001, 64), (70000, 48, 32), (40, 6000, 4096), (600, 640, 4112),
 ]
 
 
@@ -128,6 +128,17 @@ def test_neighbouring_memory_stays(q4, m, n, k):
         assert bool((buf[:128] == 7).all()) and bool((buf[128 + m * n:] == 7).all())
         q4.q8_linear_w8a8_gated(xq, sa, wg, sg, wu, su, h=y)
         assert bool((buf[:128] == 7).all()) and bool((buf[128 + m * n:] == 7).all())
+
+
+def test_outputs_past_32_bits(q4):
+    """More than 2^31 outputs: the last rows are where they belong, on both kernels' store paths (n off and on 16 bytes)."""
+    for m, n in ((33000, 66001), (33000, 66000)):
+        xq, sa, (w, sw), _ = _inputs(m, n, 16)
+        y = q4.q8_linear_w8a8(xq, sa, w, sw, out_dtype=torch.bfloat16)
+        for rows in (slice(0, 3), slice(m // 2, m // 2 + 3), slice(m - 3, m)):
+            ref = _prod(xq[rows], sa[rows], w, sw)
+            _check(y[rows], ref, (3.01 * U24 + 2.0 ** -8 * (1 + 4 * U24)) * ref.abs(), f"rows {rows}")
+        del y, xq, w
 
 
 def test_zero_scales_and_codes(q4):

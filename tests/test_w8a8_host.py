@@ -14,6 +14,8 @@ L = q4._lib
 @pytest.mark.parametrize("change,expect", [
     (dict(m=-1), q4.Q4_ERR_SHAPE),
     (dict(n=-1), q4.Q4_ERR_SHAPE),
+    (dict(m=q4.Q8_MAX_ROWS + 1), q4.Q4_ERR_SHAPE),
+    (dict(n=q4.Q8_MAX_ROWS + 1), q4.Q4_ERR_SHAPE),
     (dict(k=0), q4.Q4_ERR_SHAPE),
     (dict(k=24), q4.Q4_ERR_SHAPE),                       # rows would not start on 16 bytes
     (dict(k=q4.Q8_MAX_K + 16), q4.Q4_ERR_SHAPE),         # the sum could leave int32
