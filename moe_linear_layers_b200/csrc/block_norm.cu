@@ -7,7 +7,7 @@
 //   n  = r' * rstd(r') * pre_w
 //
 // HBM-bound: x and residual are read once and each output is written once; a row's values stay in registers
-// between the two reductions and the quantizer's.  One CTA per row.
+// between the two reductions and the quantizer's.
 //
 // Every elementwise step is one fp32 operation rounded to nearest, in the order written in the header, and the
 // sums of squares run in fp64 (their rounding error stays below a quarter of an fp32 ulp of rstd by nine
@@ -26,7 +26,7 @@ struct Args {
     int8_t* xq;
     float* scale_a;
     int x_dt, r_dt, w_dt, g_dt, y_dt;
-    int T, H, tokens_per_gate;
+    int T, H, tokens_per_gate;   // tokens_per_gate 0: one gate for all
     float eps, res_scale, branch_scale;
     double inv_h;
     uint64_t ones;      // the fp32 pair (1, 1)
@@ -99,13 +99,11 @@ template <int V> __device__ __forceinline__ void store(void* p, int dt, int64_t 
     }
 }
 
-constexpr int kMaxWarps = 32;
-
-// What a CTA's reductions go through, twice: a fast warp may write the next row's while a slow one still reads
-struct Red {
-    double sum[2][2][kMaxWarps];
-    uint32_t top[2][kMaxWarps];
-};
+// the gate's row of a token (T < 2^31, and a 64-bit division would be a fifth of a short row's instructions)
+__device__ __forceinline__ int64_t gate_row(const Args& a, int64_t row)
+{
+    return a.tokens_per_gate ? (int64_t)((uint32_t)row / (uint32_t)a.tokens_per_gate) : 0;
+}
 
 __device__ __forceinline__ double warp_sum(double v)
 {
@@ -114,21 +112,19 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
-// sum over the CTA (WARP: over the warp); every thread gets the same bits
-template <bool WARP> __device__ __forceinline__ double row_sum(double v, double* red)
+// sum over the CTA; every thread gets the same bits
+__device__ __forceinline__ double cta_sum(double v, double* red)
 {
     v = warp_sum(v);
-    if constexpr (WARP) return v;
     const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
     if (lane == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
     return warp_sum(lane < nw ? red[lane] : 0.0);
 }
 
-template <bool WARP> __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red)
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red)
 {
     v = __reduce_max_sync(0xffffffffu, v);
-    if constexpr (WARP) return v;
     const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
     if (lane == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
@@ -211,16 +207,16 @@ template <int V> __device__ __forceinline__ void store_codes(int8_t* p, const fl
     else *p = (int8_t)o[0];
 }
 
-// One row to a CTA of up to 1024 threads, or (WARP) to a warp of a CTA of 8: V values a load, P loads a thread.
-template <int V, int P, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Args a)
+// Rows of more than 16384 values: a CTA of up to 1024 threads a row, V values a load, P loads a thread.
+template <int V, int P>
+__global__ void __launch_bounds__(1024) block_norm_wide_kernel(const Args a)
 {
-    __shared__ Red red;
+    __shared__ double red_sum[2][32];
+    __shared__ uint32_t red_top[32];
     q4_pdl_start();
-    const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
-    if (WARP && row >= a.T) return;
+    const int64_t row = blockIdx.x;
     const int64_t base = row * a.H;
-    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    const int tid = threadIdx.x, nt = blockDim.x;
     float v[P][V], r[P][V];
     // both rows' loads go out before either is used
 #pragma unroll
@@ -235,7 +231,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Arg
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < P; i++) add_squares<V>(v[i], s);
-        const float rs = rstd_of(row_sum<WARP>(s, red.sum[0][0]), a);
+        const float rs = rstd_of(cta_sum(s, red_sum[0]), a);
 #pragma unroll
         for (int i = 0; i < P; i++) {
             const int c = (i * nt + tid) * V;
@@ -246,7 +242,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Arg
             scale_by<V>(v[i], w);
         }
     }
-    const int64_t grow = a.gate ? (row / a.tokens_per_gate) * a.H : 0;
+    const int64_t grow = a.gate ? gate_row(a, row) * a.H : 0;
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < P; i++) {
@@ -270,7 +266,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Arg
             store<V>(a.residual_out, a.r_dt, base + c, v[i]);
     }
     if (!a.y && !a.xq) return;
-    const float rs = rstd_of(row_sum<WARP>(s, red.sum[0][1]), a);
+    const float rs = rstd_of(cta_sum(s, red_sum[1]), a);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < P; i++) {
@@ -286,7 +282,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Arg
         if (a.xq) settle<V>(v[i], a.y_dt, top);
     }
     if (!a.xq) return;
-    top = row_max<WARP>(top, red.top[0]);
+    top = cta_max(top, red_top);
     const float scale = scale_of(top);
     if (tid == 0) {
         a.scale_a[row] = scale;
@@ -300,26 +296,6 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) block_norm_kernel(const Arg
         if (c < a.H && q4_in_bounds(base + c + V - 1, (int64_t)a.T * a.H, a.status))
             store_codes<V>(a.xq + base + c, v[i], scale, inv, exact_div);
     }
-}
-
-// Many rows: one persistent CTA of 16 warps an SM.  A team of W warps (1 up to 1024 values a row) owns a row at a time, E
-// values a lane in registers, so a row's two sums and its maximum cost a lane a few instructions for E values
-// and, with one warp a team, no barrier.  (With 256 threads a row the reductions alone were a fifth of 78 instructions a
-// value: 2.1 TB/s.)  Rows come ahead of use by bulk copies into the team's ring in shared memory: x, the residual, and
-// the gate's row where it changes with the token.  A copy covers the 16-byte pieces that hold the row, so rows of any width
-// and alignment take this path: V values are then read at a time (8, 2, 1), where the row allows.  What every row
-// shares (the norms' weights, a single gate) is kept as fp32 in shared memory.
-struct Ring {
-    int stages, warps, teams;        // slots a team, warps a team, teams a CTA
-    int slot[3];                     // bytes of a slot's x, residual and gate pieces (0: not in the ring)
-    int post, gate, pre;             // where the shared vectors start (bytes; -1: none)
-    int rings;                       // where the rings start
-};
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float max_nan(float a, float b)   // max(a, |b|), NaN wins
@@ -337,10 +313,6 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-
-// 64 values a lane need 128 registers, fewer fit in 100
-__host__ __device__ constexpr int team_threads(int e) { return e == 64 ? 512 : 640; }
-constexpr int kMaxSlots = 48;   // stages x teams
 
 // V values of type DT at p
 template <int V, int DT> __device__ __forceinline__ void get(const uint8_t* p, float (&v)[V])
@@ -389,6 +361,270 @@ template <typename F> __device__ __forceinline__ void by_type(int dt, F f)
     else f(std::integral_constant<int, Q4_F16>());
 }
 
+// a pair as DT holds it, and the largest magnitude so far
+template <int DT> __device__ __forceinline__ uint64_t settle_pair(uint64_t x, float& top)
+{
+    float lo = tc::f2_lo(x), hi = tc::f2_hi(x);
+    if constexpr (DT == Q4_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        const uint32_t e = *reinterpret_cast<const uint32_t*>(&h);
+        lo = __uint_as_float(e << 16);
+        hi = __uint_as_float(e & 0xFFFF0000u);
+    } else {
+        lo = as_stored(lo, DT);
+        hi = as_stored(hi, DT);
+    }
+    top = max_nan(max_nan(top, lo), hi);
+    return pair(lo, hi);
+}
+
+// store_codes' quotient and rounding, two values at a time: the codes are the low bytes of the two halves
+struct Coder {
+    uint64_t inv2, neg2, magic;
+    __device__ __forceinline__ explicit Coder(float scale)
+    {
+        const float inv = 1.0f / scale;
+        inv2 = pair(inv, inv);
+        neg2 = pair(-scale, -scale);
+        magic = pair(12582912.0f, 12582912.0f);
+    }
+    __device__ __forceinline__ uint64_t operator()(uint64_t x) const
+    {
+        const uint64_t t = f2_mul(x, inv2);
+        return tc::f2_add(tc::f2_fma(tc::f2_fma(neg2, t, x), inv2, t), magic);
+    }
+};
+
+__device__ __forceinline__ uint32_t code_bytes(uint64_t pair) { return prmt((uint32_t)pair, (uint32_t)(pair >> 32), 0x0040u); }
+
+// Raw words of V values of a 16-bit or 32-bit type, loaded before anything depends on the type
+template <int V> struct Raw {
+    uint32_t w[V];
+    __device__ __forceinline__ void load(const void* base, bool wide, int64_t at)
+    {
+        const uint32_t* p32 = static_cast<const uint32_t*>(base) + at;
+        const uint16_t* p16 = static_cast<const uint16_t*>(base) + at;
+        if constexpr (V == 8) {
+            const uint4 a = wide ? *reinterpret_cast<const uint4*>(p32) : *reinterpret_cast<const uint4*>(p16);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            if (wide) {
+                const uint4 b = *reinterpret_cast<const uint4*>(p32 + 4);
+                w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+            }
+        } else if constexpr (V == 2) {
+            if (wide) {
+                const uint2 a = *reinterpret_cast<const uint2*>(p32);
+                w[0] = a.x; w[1] = a.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t*>(p16);
+            }
+        } else {
+            w[0] = wide ? *p32 : *p16;
+        }
+    }
+    // pair j of the values (V == 1: the value and 0)
+    template <int DT> __device__ __forceinline__ uint64_t get(int j) const
+    {
+        if constexpr (V == 1) {
+            return pair(DT == Q4_F32    ? __uint_as_float(w[0])
+                        : DT == Q4_BF16 ? __uint_as_float(w[0] << 16)
+                                        : __half2float(__ushort_as_half((unsigned short)w[0])), 0.0f);
+        } else if constexpr (DT == Q4_F32) {
+            return tc::f2_pack(w[2 * j], w[2 * j + 1]);
+        } else if constexpr (DT == Q4_BF16) {
+            return tc::f2_pack(w[j] << 16, w[j] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(u32_as_h2(w[j]));
+            return pair(f.x, f.y);
+        }
+    }
+};
+
+// r * res + b, two values at a time.  The sum is a multiply-add by a one the compiler does not know: a packed product that
+// feeds a packed sum was seen to be contracted with it into one rounding (mul.rn.f32x2, add.rn.f32x2, CUDA 12.9), which
+// moves r' by more than an ulp where the residual and the branch cancel.
+__device__ __forceinline__ uint64_t add_scaled(uint64_t r, uint64_t res2, uint64_t b, const Args& a)
+{
+    return tc::f2_fma(f2_mul(r, res2), a.ones, b);
+}
+
+// Up to a few thousand rows: a team of W warps a row, 256 threads or a row a CTA, E values a lane in registers (V at a time,
+// chunks of a warp side by side).  x and the residual are loaded before either is used, the vectors come through L1.  One
+// branch on a type stands around a row's work, not around a value's, and the fp32 arithmetic is packed in pairs (a CTA of 256
+// threads with 8 values each and neither of the two took 78 instructions a value; CTAs of 128 threads instead of 256 cost 4800
+// x 2048 rows 34 us instead of 24).  FULL: the lanes' values make up the row exactly (V = 8), without bound checks.
+template <int V, int E, bool FULL>
+__global__ void __launch_bounds__(512) block_norm_row_kernel(const Args a, const int W)
+{
+    constexpr int C = E / V, Q = (V + 1) / 2, D = 32 * V;   // D: between a lane's chunks
+    __shared__ double red_sum[2][16];
+    __shared__ float red_top[16];
+    const int H = a.H, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int team = warp / W, first_warp = team * W, tl = (warp - first_warp) * 32 + lane;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 32 / W) + team;
+    q4_pdl_start();
+    if (row >= a.T) return;      // (whole teams)
+    const int64_t base = row * H;
+    const int c0 = (warp - first_warp) * (32 * E) + lane * V, left = H - c0;
+    auto each = [&](auto f) {    // f(chunk) for this lane's chunks of the row
+#pragma unroll
+        for (int i = 0; i < C; i++)
+            if (FULL || i * D < left) f(i);
+    };
+    auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * W) : "memory"); };
+    auto team_sum = [&](double v, double* red) {
+        v = warp_sum(v);
+        if (W == 1) return v;
+        if (lane == 0) red[warp] = v;
+        team_sync();
+        v = red[first_warp];
+        for (int i = 1; i < W; i++) v += red[first_warp + i];
+        return v;
+    };
+    Raw<V> rx[C], rr[C];
+    if (a.x) each([&](int i) { rx[i].load(a.x, a.x_dt == Q4_F32, base + c0 + i * D); });
+    if (a.residual) each([&](int i) { rr[i].load(a.residual, a.r_dt == Q4_F32, base + c0 + i * D); });
+    // the lane's values; what is not of the row stays 0 (-0 without x: a sum with -0 keeps every value as it is)
+    uint64_t v[C][Q];
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < C; i++)
+#pragma unroll
+            for (int j = 0; j < Q; j++) v[i][j] = f(v[i][j]);
+    };
+    auto times = [&](float f) {
+        const uint64_t f2 = pair(f, f);
+        all([&](uint64_t x) { return f2_mul(x, f2); });
+    };
+    auto times_vector = [&](const void* p, int dt) {
+        by_type(dt, [&](auto DT) {
+            each([&](int i) {
+                Raw<V> w;
+                w.load(p, DT() == Q4_F32, c0 + i * D);
+#pragma unroll
+                for (int j = 0; j < Q; j++) v[i][j] = f2_mul(v[i][j], w.template get<DT()>(j));
+            });
+        });
+    };
+    auto squares = [&] {   // four chains: one would wait for each multiply-add
+        double s4[4] = {};
+#pragma unroll
+        for (int i = 0; i < C; i++)
+#pragma unroll
+            for (int j = 0; j < Q; j++) {
+                const int k = 2 * ((i * Q + j) & 1);
+                const double lo = (double)tc::f2_lo(v[i][j]);
+                s4[k] = fma(lo, lo, s4[k]);
+                if constexpr (V > 1) {
+                    const double hi = (double)tc::f2_hi(v[i][j]);
+                    s4[k + 1] = fma(hi, hi, s4[k + 1]);
+                }
+            }
+        return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    };
+    all([&](uint64_t) { return a.x ? 0ull : 0x8000000080000000ull; });
+    if (a.x) {
+        by_type(a.x_dt, [&](auto DT) {
+            each([&](int i) {
+#pragma unroll
+                for (int j = 0; j < Q; j++) v[i][j] = rx[i].template get<DT()>(j);
+            });
+        });
+        if (a.post_w) {
+            times(rstd_of(team_sum(squares(), red_sum[0]), a));
+            times_vector(a.post_w, a.w_dt);
+        }
+        if (a.branch_scale != 1.0f) times(a.branch_scale);
+        if (a.gate) times_vector(static_cast<const uint8_t*>(a.gate) + gate_row(a, row) * H * (a.g_dt == Q4_F32 ? 4 : 2), a.g_dt);
+    }
+    if (a.residual) {
+        const uint64_t res2 = pair(a.res_scale, a.res_scale);
+        by_type(a.r_dt, [&](auto DT) {
+            each([&](int i) {
+#pragma unroll
+                for (int j = 0; j < Q; j++) v[i][j] = add_scaled(rr[i].template get<DT()>(j), res2, v[i][j], a);
+            });
+        });
+    }
+    auto chunk = [&](int i, float (&w)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; j++) w[j] = j & 1 ? tc::f2_hi(v[i][j / 2]) : tc::f2_lo(v[i][j / 2]);
+    };
+    auto write = [&](void* out, auto DT) {
+        constexpr int es = DT() == Q4_F32 ? 4 : 2;
+        uint8_t* p = static_cast<uint8_t*>(out) + (base + c0) * es;
+        each([&](int i) {
+            float w[V];
+            chunk(i, w);
+            if (q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) put<V, DT()>(p + i * (D * es), w);
+        });
+    };
+    if (a.residual_out) by_type(a.r_dt, [&](auto DT) { write(a.residual_out, DT); });
+    if (!a.y && !a.xq) return;
+    times(rstd_of(team_sum(squares(), red_sum[1]), a));
+    if (a.pre_w) times_vector(a.pre_w, a.w_dt);
+    float top = 0.0f;
+    by_type(a.y_dt, [&](auto DT) {
+        if (a.y) write(a.y, DT);
+        if (a.xq) all([&](uint64_t x) { return settle_pair<DT()>(x, top); });
+    });
+    if (!a.xq) return;
+    uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // (bit order = order of magnitudes, NaN on top)
+    if (W > 1) {
+        if (lane == 0) red_top[warp] = __uint_as_float(tb);
+        team_sync();
+        for (int i = 0; i < W; i++) tb = max(tb, __float_as_uint(red_top[first_warp + i]));
+    }
+    const float scale = scale_of(tb);
+    if (tl == 0) {
+        a.scale_a[row] = scale;
+        if (tb >= 0x7F800000u) q4_set_status(a.status, Q4_ERR_NONFINITE);
+    }
+    int8_t* out = a.xq + base + c0;
+    if (!(scale >= 0x1p-100f && scale < INFINITY)) {
+        each([&](int i) {
+            float w[V];
+            chunk(i, w);
+            if (q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) store_codes<V>(out + i * D, w, scale, 0.0f, true);
+        });
+        return;
+    }
+    const Coder code(scale);
+    each([&](int i) {
+        if (!q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) return;
+        if constexpr (V == 8)
+            *reinterpret_cast<uint2*>(out + i * D) =
+                make_uint2(prmt(code_bytes(code(v[i][0])), code_bytes(code(v[i][1])), 0x5410u),
+                           prmt(code_bytes(code(v[i][2])), code_bytes(code(v[i][3])), 0x5410u));
+        else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(out + i * D) = (uint16_t)code_bytes(code(v[i][0]));
+        else out[i * D] = (int8_t)code(v[i][0]);
+    });
+}
+
+// Many rows: one persistent CTA of 16 warps an SM.  A team of W warps (1 up to 1024 values a row) owns a row at a time, E
+// values a lane in registers, so a row's two sums and its maximum cost a lane a few instructions for E values
+// and, with one warp a team, no barrier.  (With 256 threads a row the reductions alone were a fifth of 78 instructions a
+// value: 2.1 TB/s.)  Rows come ahead of use by bulk copies into the team's ring in shared memory: x, the residual, and
+// the gate's row where it changes with the token.  A copy covers the 16-byte pieces that hold the row, so rows of any width
+// and alignment take this path: V values are then read at a time (8, 2, 1), where the row allows.  What every row
+// shares (the norms' weights, a single gate) is kept as fp32 in shared memory.
+struct Ring {
+    int stages, warps, teams;        // slots a team, warps a team, teams a CTA
+    int slot[3];                     // bytes of a slot's x, residual and gate pieces (0: not in the ring)
+    int post, gate, pre;             // where the shared vectors start (bytes; -1: none)
+    int rings;                       // where the rings start
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+// 64 values a lane need 128 registers, fewer fit in 100
+__host__ __device__ constexpr int team_threads(int e) { return e == 64 ? 512 : 640; }
+constexpr int kMaxSlots = 48;   // stages x teams
+
 // A shared vector in fp32: V == 8 keeps the two halves of each 8 values apart, so that a warp's 16-byte reads of
 // consecutive pieces touch every bank once.
 template <int V> __device__ __forceinline__ int shared_at(int c, int j, int H)
@@ -435,7 +671,7 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
         uint32_t bx = 0, br = 0, bg = 0;
         if (q.slot[0]) piece(a.x, row, a.T, xs, px, bx);
         if (q.slot[1]) piece(a.residual, row, a.T, rs_, pr, br);
-        if (q.slot[2]) piece(a.gate, row / a.tokens_per_gate, g_rows, gs, pg, bg);
+        if (q.slot[2]) piece(a.gate, gate_row(a, row), g_rows, gs, pg, bg);
         tc::mbar_arrive_expect_tx(bar, bx + br + bg);
         if (bx) bulk_load(dst, px, bx, bar);
         if (br) bulk_load(dst + q.slot[0], pr, br, bar);
@@ -499,7 +735,7 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
         const int64_t base = row * H;
         uint8_t* src = ring + (int64_t)s * slot_bytes;
         ok = ok && tc::mbar_wait(&full[team * q.stages + s], phase, a.status, &abort_flag);
-        if (V != 8 && (row >= cut[0] || row >= cut[1] || (q.slot[2] && row / a.tokens_per_gate >= cut[2]))) {
+        if (V != 8 && (row >= cut[0] || row >= cut[1] || (q.slot[2] && gate_row(a, row) >= cut[2]))) {
             // the bytes past an array's last whole piece (the end of its last row, for short rows of several)
             auto tail = [&](const void* p, int64_t i, int64_t n, int es, uint8_t* dst) {
                 const int64_t b0 = i * H * es & ~(int64_t)15, end = n * H * es & ~(int64_t)15;
@@ -509,7 +745,7 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
             };
             if (q.slot[0]) tail(a.x, row, a.T, xs, src);
             if (q.slot[1]) tail(a.residual, row, a.T, rs_, src + q.slot[0]);
-            if (q.slot[2]) tail(a.gate, row / a.tokens_per_gate, g_rows, gs, src + q.slot[0] + q.slot[1]);
+            if (q.slot[2]) tail(a.gate, gate_row(a, row), g_rows, gs, src + q.slot[0] + q.slot[1]);
             team_sync();
         }
         // the lane's E values in pairs, for the packed fp32 instructions (each half rounds like the scalar one); a
@@ -590,20 +826,16 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
             if (q.slot[2])
                 by_type(a.g_dt, [&](auto DT) {
                     constexpr int es = DT() == Q4_F32 ? 4 : 2;
-                    with(src + q.slot[0] + q.slot[1] + (row / a.tokens_per_gate * H * es & 15) + c0 * es, DT, f2_mul);
+                    with(src + q.slot[0] + q.slot[1] + (gate_row(a, row) * H * es & 15) + c0 * es, DT, f2_mul);
                 });
             else if (q.gate >= 0) times_shared(s_gate);
         }
         if (q.slot[1]) {
-            // The sum is a multiply-add by a one the compiler does not know: a packed product that feeds a packed sum was
-            // seen to be contracted with it into one rounding (mul.rn.f32x2, add.rn.f32x2, CUDA 12.9), which moves r' by
-            // more than an ulp where the residual and the branch cancel.  (Without x the sum is with -0, which leaves every
-            // value, -0 among them, as it is.)
             const uint64_t rs2 = pair(a.res_scale, a.res_scale);
             by_type(a.r_dt, [&](auto DT) {
                 constexpr int es = DT() == Q4_F32 ? 4 : 2;
                 with(src + q.slot[0] + (base * es & 15) + c0 * es, DT,
-                     [&](uint64_t x, uint64_t r) { return tc::f2_fma(f2_mul(r, rs2), a.ones, x); });
+                     [&](uint64_t x, uint64_t r) { return add_scaled(r, rs2, x, a); });
             });
         }
         const float rs = rstd_of(team_sum(squares(), red_sum[par][1]), a);
@@ -636,21 +868,7 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
         float top = 0.0f;
         by_type(a.y_dt, [&](auto DT) {
             if (a.y) write(a.y, DT);
-            if (a.xq)
-                all([&](uint64_t x) {
-                    float lo = tc::f2_lo(x), hi = tc::f2_hi(x);
-                    if constexpr (DT() == Q4_BF16) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-                        const uint32_t e = *reinterpret_cast<const uint32_t*>(&h);
-                        lo = __uint_as_float(e << 16);
-                        hi = __uint_as_float(e & 0xFFFF0000u);
-                    } else {
-                        lo = as_stored(lo, DT());
-                        hi = as_stored(hi, DT());
-                    }
-                    top = max_nan(max_nan(top, lo), hi);
-                    return pair(lo, hi);
-                });
+            if (a.xq) all([&](uint64_t x) { return settle_pair<DT()>(x, top); });
         });
         if (!a.xq) continue;
         uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // (bit order = order of magnitudes, NaN on top)
@@ -673,16 +891,11 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
                 if (q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) store_codes<V>(out + i * D, w, scale, 0.0f, true);
             });
         } else {
-            // the quotient and the rounding of store_codes, two values at a time
-            const float inv = 1.0f / scale;
-            const uint64_t inv2 = pair(inv, inv), neg2 = pair(-scale, -scale), magic = pair(12582912.0f, 12582912.0f);
-            all([&](uint64_t x) {
-                const uint64_t t = f2_mul(x, inv2);
-                return tc::f2_add(tc::f2_fma(tc::f2_fma(neg2, t, x), inv2, t), magic);
-            });
+            const Coder code(scale);
+            all([&](uint64_t x) { return code(x); });
             each([&](int i) {
                 if (!q4_in_bounds(base + c0 + i * D + V - 1, (int64_t)a.T * H, a.status)) return;
-                auto bytes = [&](int j) { return prmt((uint32_t)v[j], (uint32_t)(v[j] >> 32), 0x0040u); };   // a pair's codes
+                auto bytes = [&](int j) { return code_bytes(v[j]); };
                 if constexpr (V == 8)
                     *reinterpret_cast<uint2*>(out + i * D) = make_uint2(prmt(bytes(4 * i), bytes(4 * i + 1), 0x5410u),
                                                                         prmt(bytes(4 * i + 2), bytes(4 * i + 3), 0x5410u));
@@ -697,27 +910,27 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
     }
 }
 
-template <int V> int launch_rows(const Args& a, cudaStream_t s)
+int launch_rows(const Args& a, bool whole, cudaStream_t s)
 {
-    const int words = (a.H + V - 1) / V;
-    // a warp a row while that leaves a lane at most 32 values (no barrier; a CTA for each would hold few rows an SM)
-    if (words <= 32 * (32 / V)) {
-        const dim3 grid((unsigned)((a.T + (int64_t)7) / 8)), block(256);
-        if (words <= 32) return q4_launch_pdl(block_norm_kernel<V, 1, true>, grid, block, 0, s, a);
-        if (words <= 64) return q4_launch_pdl(block_norm_kernel<V, 2, true>, grid, block, 0, s, a);
-        if constexpr (V == 8) return q4_launch_pdl(block_norm_kernel<V, 4, true>, grid, block, 0, s, a);
-        else if (words <= 256) return q4_launch_pdl(block_norm_kernel<V, 8, true>, grid, block, 0, s, a);
+    const int V = !whole || a.H % 2 ? 1 : a.H % 8 ? 2 : 8;
+    if (a.H > 16384) {
+        const dim3 grid(a.T), block(1024);
+        return V == 8 ? q4_launch_pdl(block_norm_wide_kernel<8, 4>, grid, block, 0, s, a)
+                      : q4_launch_pdl(block_norm_wide_kernel<1, 32>, grid, block, 0, s, a);
     }
-    const int p = (words + 1023) / 1024;
-    const dim3 grid(a.T), block(p > 1 ? 1024 : (words + 31) / 32 * 32);
-    if (p <= 1) return q4_launch_pdl(block_norm_kernel<V, 1, false>, grid, block, 0, s, a);
-    if (p <= 2) return q4_launch_pdl(block_norm_kernel<V, 2, false>, grid, block, 0, s, a);
-    if (p <= 4) return q4_launch_pdl(block_norm_kernel<V, 4, false>, grid, block, 0, s, a);
-    if constexpr (V == 1) {
-        if (p <= 16) return q4_launch_pdl(block_norm_kernel<V, 16, false>, grid, block, 0, s, a);
-        return q4_launch_pdl(block_norm_kernel<V, 32, false>, grid, block, 0, s, a);
-    }
-    return Q4_ERR_SHAPE;
+    // values a lane: 8 in rows of up to 256 (and one at a time: 16 take 92 registers), else 16; 16 warps a row at most
+    int E = a.H <= 256 || V == 1 ? 8 : 16;
+    while (32 * E * 16 < a.H) E *= 2;
+    const int W = (a.H + 32 * E - 1) / (32 * E), teams = std::max(1, 8 / W);
+    const dim3 grid((unsigned)((a.T + (int64_t)teams - 1) / teams)), block(32 * W * teams);
+    auto go = [&](auto kern) { return q4_launch_pdl(kern, grid, block, 0, s, a, W); };
+    if (V == 8 && a.H == 32 * E * W)
+        return E == 8 ? go(block_norm_row_kernel<8, 8, true>) : E == 16 ? go(block_norm_row_kernel<8, 16, true>) : go(block_norm_row_kernel<8, 32, true>);
+    if (V == 8)
+        return E == 8 ? go(block_norm_row_kernel<8, 8, false>) : E == 16 ? go(block_norm_row_kernel<8, 16, false>) : go(block_norm_row_kernel<8, 32, false>);
+    if (V == 2)
+        return E == 8 ? go(block_norm_row_kernel<2, 8, false>) : E == 16 ? go(block_norm_row_kernel<2, 16, false>) : go(block_norm_row_kernel<2, 32, false>);
+    return E == 8 ? go(block_norm_row_kernel<1, 8, false>) : E == 16 ? go(block_norm_row_kernel<1, 16, false>) : go(block_norm_row_kernel<1, 32, false>);
 }
 
 int elem_bytes(int dt) { return dt == Q4_F32 ? 4 : 2; }
@@ -765,23 +978,26 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
     return E == 32 ? go(block_norm_team_kernel<1, 32, false>) : go(block_norm_team_kernel<1, 16, false>);
 }
 
-// When there are rows enough for the persistent form, measured against a CTA or a warp a row (us, bf16, every part):
-//   H 256: 12000 rows 16.7 / 10.5 (a warp a row has no ring to fill: never)     H 512: 1200 rows 5.3 / 6.3
-//   H 1000: 600 rows 8.2 / 10.3     H 1001: 600 rows 11.8 / 11.9, 4800 rows 22.6 / 74.8
-//   H 2048: 1200 rows 11.3 / 10.7, 4800 rows 25.0 / 29.7     H 8192: 300 rows 12.9 / 15.9, 4800 rows 70 / 165
-// The most values a lane that leave each team two rows and the lanes four fifths full come first (long rows of few lanes
-// cost the fewest instructions); with fewer rows, more warps share one.
+// When there are rows enough for the persistent form, measured against a team a row (us, bf16, every part, persistent /
+// team a row):
+//   H 512: 12000 rows 16.0 / 14.1 (never below 1024)    H 1000: 4800 rows 18.6 / 15.2, 12000 rows 30.1 / 30.4
+//   H 2048: 4800 rows 25.1 / 24.1, 12000 rows 44.8 / 53.6    H 4096: 2400 rows 26.2 / 25.6, 4800 rows 39.7 / 46.3
+//   H 8192: 600 rows 20.8 / 18.0, 1200 rows 28.3 / 30.0, 4800 rows 70 / 102
+//   H 1001 (a value at a time): 600 rows 11.7 / 9.1, 1200 rows 12.2 / 14.9, 12000 rows 47 / 68
+// So: three rows a team (two above 4096 values), and from six rows an SM on where rows are off 16 bytes.  The most values a
+// lane that leave the lanes four fifths full cost the fewest instructions.
 int launch_many(const Args& a, bool many_gates, cudaStream_t s)
 {
-    if (a.H <= 256) return Q4_ERR_UNSUPPORTED;
-    int rc = Q4_ERR_UNSUPPORTED;
-    for (int E = 64; E >= 16 && rc == Q4_ERR_UNSUPPORTED; E /= 2) {
-        const int cap = (a.H + 32 * E - 1) / (32 * E) * 32 * E;
-        if (5 * a.H >= 4 * cap || E == 16) rc = launch_teams(a, E, 2, many_gates, s);
+    if (a.H % 8) {
+        if (a.H <= 256 || a.T < 6 * q4_num_sms()) return Q4_ERR_UNSUPPORTED;
+        return launch_teams(a, a.H <= 512 ? 16 : 32, 0, many_gates, s);
     }
-    if (rc != Q4_ERR_UNSUPPORTED) return rc;
-    if (a.H <= 1024 || a.H % 8) return a.T >= 4 * q4_num_sms() ? launch_teams(a, a.H <= 512 ? 16 : 32, 0, many_gates, s) : rc;
-    return a.H > 4096 ? launch_teams(a, 16, 1, many_gates, s) : rc;
+    if (a.H < 1024) return Q4_ERR_UNSUPPORTED;
+    for (int E = 64; E >= 16; E /= 2) {
+        const int cap = (a.H + 32 * E - 1) / (32 * E) * 32 * E;
+        if (5 * a.H >= 4 * cap || E == 16) return launch_teams(a, E, a.H > 4096 ? 2 : 3, many_gates, s);
+    }
+    return Q4_ERR_UNSUPPORTED;
 }
 
 // two arrays share memory (NULL shares none)
@@ -847,7 +1063,7 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
     a.y_dt = d->y_dtype;
     a.T = T;
     a.H = H;
-    a.tokens_per_gate = d->gate ? T / d->gate_rows : 1;
+    a.tokens_per_gate = d->gate && d->gate_rows > 1 ? T / d->gate_rows : 0;
     a.eps = d->eps;
     a.res_scale = d->res_scale;
     a.branch_scale = d->branch_scale;
@@ -855,7 +1071,7 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
     a.ones = 0x3F8000003F800000ull;
     a.status = dev_status;
     // Arrays that start on 16 bytes (8 for the codes) take the persistent form when there are rows enough, and
-    // 16-byte accesses when H % 8 == 0 keeps the rows so; anything else goes one value at a time.
+    // 16-byte accesses when H % 8 == 0 keeps the rows so (pairs when H is even); anything else goes one value at a time.
     const bool whole = q4_aligned16(d->x) && q4_aligned16(d->residual) && q4_aligned16(d->residual_out) &&
                        q4_aligned16(d->post_w) && q4_aligned16(d->pre_w) && q4_aligned16(d->gate) && q4_aligned16(d->y) &&
                        ((uintptr_t)d->xq & 7u) == 0;
@@ -863,5 +1079,5 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
         const int rc = launch_many(a, d->gate && d->gate_rows > 1, (cudaStream_t)stream);
         if (rc != Q4_ERR_UNSUPPORTED) return rc;
     }
-    return whole && H % 8 == 0 ? launch_rows<8>(a, (cudaStream_t)stream) : launch_rows<1>(a, (cudaStream_t)stream);
+    return launch_rows(a, whole, (cudaStream_t)stream);
 }
