@@ -5,6 +5,9 @@
 
 namespace w8 {
 
+// The kernels start while the previous one on the stream still runs (programmatic dependent launch) and read what it may
+// write only behind their wait; those are plain loads, since a read-only (.nc) load promises that the data does not change
+// while the kernel lives.
 struct Problem {
     const int8_t* xq;        // [m][k]
     const float* scale_a;    // [m]

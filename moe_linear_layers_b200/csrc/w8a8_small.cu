@@ -7,7 +7,8 @@
 // block of rows g and g + 8 (weights) and of token g (activations), and the four words fill two MMAs' slots.
 //
 // Memory-bound: n * k bytes of weights.  The CTA's warps split k in 128-byte blocks, and meet
-// once through shared memory.
+// once through shared memory.  Measured on B200, back to back: 1 x 2048 x 2048 2.3 us, 1 x 8192 x 2048 3.2 us (5.2 TB/s, weights
+// partly in L2), gated 8.1 us (4.1 TB/s), 16 x 2048 x 8192 6.4 us.
 #include "w8a8_common.cuh"
 
 namespace {
@@ -25,7 +26,7 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 
 __device__ __forceinline__ uint4 ld16(const int8_t* p, bool ok)
 {
-    return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+    return ok ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // MT: groups of 8 tokens a CTA; MATS: 1, or 2 = gate and up; U: blocks of k whose loads are in flight together
@@ -95,10 +96,10 @@ __global__ void __launch_bounds__(kWarps * 32) w8a8_small_kernel(const Problem p
         for (int q = 0; q < MATS; q++)
 #pragma unroll
             for (int w = 0; w < kWarps; w++) s[q] += part[w][q * 8 * MT * kRows + o];
-        const float sa = __ldg(p.scale_a + j);
-        float v = w8::rescale(s[0], __ldg(p.scale_0 + n), sa);
-        if constexpr (MATS == 2) v = w8::gated(v, w8::rescale(s[1], __ldg(p.scale_1 + n), sa), p.act);
-        else if (p.bias) v = __fadd_rn(v, __ldg(p.bias + n));
+        const float sa = p.scale_a[j];
+        float v = w8::rescale(s[0], p.scale_0[n], sa);
+        if constexpr (MATS == 2) v = w8::gated(v, w8::rescale(s[1], p.scale_1[n], sa), p.act);
+        else if (p.bias) v = __fadd_rn(v, p.bias[n]);
         const int64_t at = (int64_t)j * p.n + n;
         if (!q4_in_bounds(at, (int64_t)p.m * p.n, p.status)) continue;
         if (p.out_bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
