@@ -33,7 +33,7 @@ namespace {
 //
 // The other two by what was measured on B200 (16 and 64 blocks of K, 8 to 1024 tokens), in us:
 //   split: 3.3 + bn / (36 splits) + bn / 128 for the exchange + 0.24 to 0.43 a block of K, for each wave of CTAs
-//   pair:  4.7 + 0.27 a block of K a wave, and 3 more from the second wave on
+//   pair:  5.3 + 0.27 a block of K a wave, and 3 more from the second wave on
 // (2048 x 8192, 65 tokens: split 9.2, pair 22.4; 2048 x 2048, 512 tokens: 9.2 / 9.9; 8192 x 2048, 256 tokens: 13.3 / 10.5.)
 struct Choice {
     int bn, splits;   // bn 0: the pair kernel
@@ -45,7 +45,7 @@ Choice choose(const w8::Problem& p)
     const int kb = (p.k + 127) / 128, sms = q4_num_sms();
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t pair_waves = ceil_div(ceil_div(p.m, 256) * ceil_div(p.n, gated ? 128 : 256), sms / 2);
-    double best = 4.7 + 0.27 * kb * pair_waves + 3.0 * (pair_waves - 1);
+    double best = 5.3 + 0.27 * kb * pair_waves + 3.0 * (pair_waves - 1);
     Choice c = {0, 1};
     const int64_t tiles_n = ceil_div(p.n, gated ? 64 : 128);
     for (int i = 0; i < 4; i++) {

@@ -267,7 +267,7 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 __syncwarp();
             }
         }
-        if (lane == 0) w8::bulk_wait_read<0>();   // (the grid's completion covers the writes)
+        if (lane == 0) w8::bulk_wait_all();   // the output is written before the grid can count as complete
     }
     tc::fence_before_sync();
     __syncwarp();
