@@ -1,6 +1,6 @@
 /*
- * q4.h -- C ABI of the group-wise INT4 linear layers and the INT4 MoE expert FFN for NVIDIA B200
- * (sm_100a).  Library: moe_linear_layers_b200/libq4.so.
+ * q4.h -- C ABI of the group-wise INT4 linear layers, the INT4 MoE expert FFN and the INT8 layers beside them for
+ * NVIDIA B200 (sm_100a).  Library: moe_linear_layers_b200/libq4.so.
  *
  * The calls follow the problem as the source pages state it:
  *   - "MoE推理优化实战：4bit存储+INT8计算的W4A8路线解析" (below: the W4A8 page) §2.3: weights are
@@ -334,7 +334,8 @@ typedef struct q4_block_norm {
     float* scale_a;
     int32_t x_dtype, residual_dtype, w_dtype, gate_dtype, y_dtype;
     int32_t gate_rows;
-    float eps, res_scale, branch_scale;
+    double eps;
+    float res_scale, branch_scale;
 } q4_block_norm;
 int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t* dev_status, void* stream);
 

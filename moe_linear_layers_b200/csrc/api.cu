@@ -41,7 +41,7 @@ extern "C" const char* q4_status_string(int status)
     }
 }
 
-extern "C" int q4_version(void) { return 1; }
+extern "C" int q4_version(void) { return 2; }
 
 extern "C" int q4_build_flags(void)
 {

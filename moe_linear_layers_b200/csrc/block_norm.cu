@@ -27,8 +27,8 @@ struct Args {
     float* scale_a;
     int x_dt, r_dt, w_dt, g_dt, y_dt;
     int T, H, tokens_per_gate;   // tokens_per_gate 0: one gate for all
-    float eps, res_scale, branch_scale;
-    double inv_h;
+    float res_scale, branch_scale;
+    double eps, inv_h;
     uint64_t ones;      // the fp32 pair (1, 1)
     int32_t* status;
 };
@@ -139,7 +139,7 @@ template <int V> __device__ __forceinline__ void add_squares(const float (&v)[V]
 
 __device__ __forceinline__ float rstd_of(double sum, const Args& a)
 {
-    const double m = fma(sum, a.inv_h, (double)a.eps);
+    const double m = fma(sum, a.inv_h, a.eps);
     if (m > 1e-30 && m < 1e30) {
         // the fp32 root (off by a relative d of 2^-22 or so) and one third-order step in fp64: off by d^3, and a
         // fraction of the fp64 root's instructions, which every warp of a row would issue
@@ -1019,7 +1019,7 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
     if (!known_dtype(d->x_dtype) || !known_dtype(d->residual_dtype) || !known_dtype(d->w_dtype) ||
         !known_dtype(d->gate_dtype) || !known_dtype(d->y_dtype))
         return Q4_ERR_UNSUPPORTED;
-    if (!(d->eps >= 0.0f) || isinf(d->eps)) return Q4_ERR_SHAPE;
+    if (!(d->eps >= 0.0) || isinf(d->eps)) return Q4_ERR_SHAPE;
     if (d->gate && (d->gate_rows < 1 || T % d->gate_rows)) return Q4_ERR_SHAPE;
     if (T == 0) return Q4_OK;   // no rows: the arrays hold nothing and may be NULL
     if (!d->x && !d->residual) return Q4_ERR_NULL;

@@ -61,7 +61,8 @@ _i32, _p, _sz = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 class q4_block_norm(ctypes.Structure):
     _fields_ = [(f, _p) for f in ("x", "residual", "post_w", "gate", "pre_w", "residual_out", "y", "xq", "scale_a")] + \
                [(f, _i32) for f in ("x_dtype", "residual_dtype", "w_dtype", "gate_dtype", "y_dtype", "gate_rows")] + \
-               [(f, ctypes.c_float) for f in ("eps", "res_scale", "branch_scale")]
+               [("eps", ctypes.c_double)] + \
+               [(f, ctypes.c_float) for f in ("res_scale", "branch_scale")]
 
 
 _lib.q4_status_string.restype = ctypes.c_char_p
@@ -118,7 +119,7 @@ _lib.q8_linear_w8a8.argtypes = [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, 
 _lib.q8_linear_w8a8_gated.argtypes = [_p, _p, _i32, _p, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p]
 _lib.block_norm.argtypes = [_p, _i32, _i32, _p, _p]
 # a q4_block_norm from its fields in order, at a sixth of the cost of filling the ctypes structure
-_pack_block_norm = struct.Struct("9Q6i3f4x").pack
+_pack_block_norm = struct.Struct("9Q6id2f").pack
 
 
 class Q4Error(RuntimeError):

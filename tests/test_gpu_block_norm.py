@@ -39,7 +39,7 @@ def _case(T, H, xd, rd, wd, gd, post, gates, seed=0, with_x=True, with_res=True,
 def _steps(c, eps, rs, bs, ydt):
     """The documented steps: one fp32 operation each."""
     one = np.float32
-    rstd = lambda v: (1.0 / np.sqrt(np.square(v.astype(np.float64)).mean(1, keepdims=True) + np.float64(one(eps)))).astype(one)  # noqa: E731
+    rstd = lambda v: (1.0 / np.sqrt(np.square(v.astype(np.float64)).mean(1, keepdims=True) + eps)).astype(one)  # noqa: E731
     with np.errstate(all="ignore"):
         b = c["x"]
         if b is not None:
@@ -98,7 +98,7 @@ def _check(q4, T, H, xd=BF16, rd=BF16, wd=F32, gd=F32, yd=BF16, post=True, gates
         assert xq is None and sa is None
     # the formula in 64 bits
     d = {k: None if v is None else v.astype(np.float64) for k, v in c.items()}
-    rstd = lambda v: 1.0 / np.sqrt((v * v).mean(1, keepdims=True) + float(np.float32(eps)))  # noqa: E731
+    rstd = lambda v: 1.0 / np.sqrt((v * v).mean(1, keepdims=True) + eps)  # noqa: E731
     b = np.zeros((T, H))
     if d["x"] is not None:
         b = d["x"] * (rstd(d["x"]) * d["post_w"] if post else 1.0) * float(np.float32(bs))
@@ -174,6 +174,20 @@ def test_in_place_and_single_outputs(q4, T, H):
     res, x = t["residual"].clone(), t["x"].clone()
     out, yy, q, s = q4.block_norm(x, res, t["pre_w"], residual_out=res, y=x, quant=True, **args)
     assert out is res and yy is x and torch.equal(res, r) and torch.equal(x, y) and torch.equal(q, xq) and torch.equal(s, sa)
+
+
+def test_eps_in_64_bits(q4):
+    """eps counts with all its digits: a mean square next to a rounding border of rstd shows one rounded to fp32."""
+    H, eps = 128, 1e-5
+    g = np.random.default_rng(7)
+    x = g.standard_normal((200000, H)).astype(np.float32)
+    ms = np.square(x.astype(np.float64)).mean(1)
+    off = (1 / np.sqrt(ms + eps)).astype(np.float32) != (1 / np.sqrt(ms + float(np.float32(eps)))).astype(np.float32)
+    rows = np.concatenate([x[off], x[:50]])
+    assert off.any()
+    _, y, _, _ = q4.block_norm(torch.from_numpy(rows).cuda(), None, None, eps=eps, out_dtype=F32, want_residual=False)
+    want = rows * (1 / np.sqrt(np.square(rows.astype(np.float64)).mean(1, keepdims=True) + eps)).astype(np.float32)
+    assert np.array_equal(y.cpu().numpy(), want)
 
 
 def test_rows_past_32_bits(q4):

@@ -100,6 +100,14 @@ def test_block_norm_validation(change, T, H, expect):
     assert L.block_norm(ctypes.byref(d), T, H, None, None) == expect
 
 
+def test_packed_descriptor_is_the_structure():
+    """The binding's one-call packing and the ctypes structure lay out the same bytes."""
+    vals = [*range(101, 110), 0, 1, 2, 0, 1, 5, 1e-5, 0.5, 0.25]
+    packed = q4._pack_block_norm(*vals)
+    d = q4.q4_block_norm(*vals)
+    assert packed == bytes(d) and len(packed) == ctypes.sizeof(d) == 112
+
+
 def test_block_norm_null_descriptor():
     assert L.block_norm(None, 4, 64, None, None) == q4.Q4_ERR_NULL
 
