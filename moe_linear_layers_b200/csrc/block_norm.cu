@@ -314,31 +314,8 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
     return d;
 }
 
-// V values of type DT at p
-template <int V, int DT> __device__ __forceinline__ void get(const uint8_t* p, float (&v)[V])
-{
-    if constexpr (V == 8) {
-        load<8>(p, DT, 0, v);
-    } else if constexpr (V == 2) {
-        if constexpr (DT == Q4_F32) {
-            const float2 a = *reinterpret_cast<const float2*>(p);
-            v[0] = a.x;
-            v[1] = a.y;
-        } else {
-            const uint32_t e = *reinterpret_cast<const uint32_t*>(p);
-            if constexpr (DT == Q4_BF16) {
-                v[0] = __uint_as_float(e << 16);
-                v[1] = __uint_as_float(e & 0xFFFF0000u);
-            } else {
-                const float2 f = __half22float2(u32_as_h2(e));
-                v[0] = f.x;
-                v[1] = f.y;
-            }
-        }
-    } else {
-        load<1>(p, DT, 0, v);
-    }
-}
+// V values (8 or 1) of type DT at p
+template <int V, int DT> __device__ __forceinline__ void get(const uint8_t* p, float (&v)[V]) { load<V>(p, DT, 0, v); }
 
 template <int V, int DT> __device__ __forceinline__ void put(uint8_t* p, const float (&v)[V])
 {
@@ -605,8 +582,8 @@ __global__ void __launch_bounds__(512) block_norm_row_kernel(const Args a, const
 // values a lane in registers, so a row's two sums and its maximum cost a lane a few instructions for E values
 // and, with one warp a team, no barrier.  (With 256 threads a row the reductions alone were a fifth of 78 instructions a
 // value: 2.1 TB/s.)  Rows come ahead of use by bulk copies into the team's ring in shared memory: x, the residual, and
-// the gate's row where it changes with the token.  A copy covers the 16-byte pieces that hold the row, so rows of any width
-// and alignment take this path: V values are then read at a time (8, 2, 1), where the row allows.  What every row
+// the gate's row where it changes with the token.  A copy covers the 16-byte pieces that hold the row, so rows of odd
+// width take this path too, one value at a time (V = 1; else V = 8).  What every row
 // shares (the norms' weights, a single gate) is kept as fp32 in shared memory.
 struct Ring {
     int stages, warps, teams;        // slots a team, warps a team, teams a CTA
@@ -899,7 +876,6 @@ __global__ void __launch_bounds__(team_threads(E), 1) block_norm_team_kernel(con
                 if constexpr (V == 8)
                     *reinterpret_cast<uint2*>(out + i * D) = make_uint2(prmt(bytes(4 * i), bytes(4 * i + 1), 0x5410u),
                                                                         prmt(bytes(4 * i + 2), bytes(4 * i + 3), 0x5410u));
-                else if constexpr (V == 2) *reinterpret_cast<uint16_t*>(out + i * D) = (uint16_t)bytes(i);
                 else out[i * D] = (int8_t)(i & 1 ? v[i / 2] >> 32 : v[i / 2]);
             });
         }
@@ -939,7 +915,7 @@ int elem_bytes(int dt) { return dt == Q4_F32 ? 4 : 2; }
 int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream_t s)
 {
     const int sms = q4_num_sms();
-    const int V = a.H % 8 == 0 ? 8 : a.H % 2 == 0 ? 2 : 1;
+    const int V = a.H % 8 == 0 ? 8 : 1;
     Ring q = {};
     q.warps = (a.H + 32 * E - 1) / (32 * E);
     if (q.warps > team_threads(E) / 32) return Q4_ERR_UNSUPPORTED;
@@ -974,7 +950,6 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
     if (V == 8) return E == 64 ? go(block_norm_team_kernel<8, 64, false>) : E == 32 ? go(block_norm_team_kernel<8, 32, false>)
                                                                                     : go(block_norm_team_kernel<8, 16, false>);
     if (E == 64) return Q4_ERR_UNSUPPORTED;   // (spills)
-    if (V == 2) return E == 32 ? go(block_norm_team_kernel<2, 32, false>) : go(block_norm_team_kernel<2, 16, false>);
     return E == 32 ? go(block_norm_team_kernel<1, 32, false>) : go(block_norm_team_kernel<1, 16, false>);
 }
 
@@ -983,15 +958,17 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
 //   H 512: 12000 rows 16.0 / 14.1 (never below 1024)    H 1000: 4800 rows 18.6 / 15.2, 12000 rows 30.1 / 30.4
 //   H 2048: 4800 rows 25.1 / 24.1, 12000 rows 44.8 / 53.6    H 4096: 2400 rows 26.2 / 25.6, 4800 rows 39.7 / 46.3
 //   H 8192: 600 rows 20.8 / 18.0, 1200 rows 28.3 / 30.0, 4800 rows 70 / 102
-//   H 1001 (a value at a time): 600 rows 11.7 / 9.1, 1200 rows 12.2 / 14.9, 12000 rows 47 / 68
-// So: three rows a team (two above 4096 values), and from six rows an SM on where rows are off 16 bytes.  The most values a
-// lane that leave the lanes four fifths full cost the fewest instructions.
+//   H 1001 (a value at a time): 1111 rows 12.2 / 7.9, 1600 rows 12.5 / 11.9, 2400 rows 12.8 / 16.4, 9600 rows 39 / 51
+//   H 5001: 900 rows 26 / 48    H 1002 (pairs): 1111 rows 12.0 / 7.3, 9600 rows 40 / 29 (never)
+// So: three rows a team (two above 4096 values); rows of odd width from 12 an SM (4 above 4096 values) on; rows of pairs not at
+// all.  The most values a lane that leave the lanes four fifths full cost the fewest instructions.
 int launch_many(const Args& a, bool many_gates, cudaStream_t s)
 {
-    if (a.H % 8) {
-        if (a.H <= 256 || a.T < 6 * q4_num_sms()) return Q4_ERR_UNSUPPORTED;
+    if (a.H % 2) {
+        if (a.H <= 256 || a.T < (a.H > 4096 ? 4 : 12) * q4_num_sms()) return Q4_ERR_UNSUPPORTED;
         return launch_teams(a, a.H <= 512 ? 16 : 32, 0, many_gates, s);
     }
+    if (a.H % 8) return Q4_ERR_UNSUPPORTED;
     if (a.H < 1024) return Q4_ERR_UNSUPPORTED;
     for (int E = 64; E >= 16; E /= 2) {
         const int cap = (a.H + 32 * E - 1) / (32 * E) * 32 * E;
