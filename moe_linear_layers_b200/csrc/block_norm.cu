@@ -961,7 +961,7 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
 //   H 1001 (a value at a time): 1111 rows 12.2 / 7.9, 1600 rows 12.5 / 11.9, 2400 rows 12.8 / 16.4, 9600 rows 39 / 51
 //   H 5001: 900 rows 26 / 48    H 1002 (pairs): 1111 rows 12.0 / 7.3, 9600 rows 40 / 29 (never)
 // So: three rows a team (two above 4096 values); rows of odd width from 12 an SM (4 above 4096 values) on; rows of pairs not at
-// all.  The most values a lane that leave the lanes four fifths full cost the fewest instructions.
+// all.  The most values a lane that make up the row, or else leave the lanes four fifths full, cost the fewest instructions.
 int launch_many(const Args& a, bool many_gates, cudaStream_t s)
 {
     if (a.H % 2) {
@@ -970,6 +970,9 @@ int launch_many(const Args& a, bool many_gates, cudaStream_t s)
     }
     if (a.H % 8) return Q4_ERR_UNSUPPORTED;
     if (a.H < 1024) return Q4_ERR_UNSUPPORTED;
+    // (5120 values: 32 a lane make up the row, 9600 rows 95 us; 64 fill it to five sixths, 104)
+    const int full = a.H % 2048 == 0 ? 64 : a.H % 1024 == 0 ? 32 : 0;
+    if (full) return launch_teams(a, full, a.H > 4096 ? 2 : 3, many_gates, s);
     for (int E = 64; E >= 16; E /= 2) {
         const int cap = (a.H + 32 * E - 1) / (32 * E) * 32 * E;
         if (5 * a.H >= 4 * cap || E == 16) return launch_teams(a, E, a.H > 4096 ? 2 : 3, many_gates, s);
