@@ -248,20 +248,27 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     }
                 } else if (any) {
                     __syncwarp();
-                    // rows that do not start on 16 bytes: a warp stores 32 columns of a row at a time
+                    // rows that do not start on 16 bytes: a warp stores 32 columns of a row at a time, or 32 pairs of bf16
+                    // columns where the rows start on 4 bytes
                     constexpr int ES = OUT32 ? 4 : 2;
                     const int rows = min(32, p.m - m0);
-                    for (int x = lane; x < W; x += 32) {
-                        if (nc + x >= p.n) continue;
+                    auto columns = [&](int x, auto WORD) {
+                        using Word = decltype(WORD);
                         const int piece = x * ES >> 4, inner = x * ES & 15;
                         uint8_t* dst = static_cast<uint8_t*>(p.y) + ((int64_t)m0 * p.n + nc + x) * ES;
 #pragma unroll 8
                         for (int i = 0; i < rows; i++, dst += (int64_t)p.n * ES) {
-                            const uint8_t* src = stage + i * 128 + ((piece ^ (i & 7)) << 4) + inner;
-                            if (!q4_in_bounds((int64_t)(m0 + i) * p.n + nc + x, (int64_t)p.m * p.n, p.status)) continue;
-                            if constexpr (OUT32) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
-                            else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+                            if (!q4_in_bounds((int64_t)(m0 + i) * p.n + nc + x + (int)sizeof(Word) / ES - 1, (int64_t)p.m * p.n, p.status)) continue;
+                            *reinterpret_cast<Word*>(dst) = *reinterpret_cast<const Word*>(stage + i * 128 + ((piece ^ (i & 7)) << 4) + inner);
                         }
+                    };
+                    if constexpr (OUT32) {
+                        if (nc + lane < p.n) columns(lane, uint32_t());
+                    } else if (p.n % 2 == 0) {
+                        if (nc + 2 * lane < p.n) columns(2 * lane, uint32_t());
+                    } else {
+                        for (int x = lane; x < W; x += 32)
+                            if (nc + x < p.n) columns(x, uint16_t());
                     }
                 }
                 __syncwarp();
