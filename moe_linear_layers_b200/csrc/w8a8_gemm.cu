@@ -165,20 +165,28 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         uint8_t* stage = out_stage + e * kStageOut;
         uint32_t tl = 0;
         bool ok = true;   // (a warp that gave up still meets the others at the barriers)
+        // a tile's channel scales and biases, one a thread (256 epilogue threads, 256 columns), and its lane's token scale come
+        // a tile ahead (4096 x 8192 x 512: 28.8 -> 28.1 us; the outputs alone, 67 MB, take 20 us at the rate of writes)
+        float next_sw = 0.0f, next_bias = 0.0f, next_sa = 0.0f;
+        auto fetch = [&](int t) {
+            if (t >= g.tiles) return;
+            const int m = (t % g.tiles_m) * (2 * BM) + (int)rank * BM + 32 * q + lane;
+            const int c = threadIdx.x - 128, n = (t / g.tiles_m) * ROWS + (GATED ? c % BNC : c);
+            next_sw = n < p.n ? (GATED && c >= BNC ? p.scale_1 : p.scale_0)[n] : 0.0f;
+            if (!GATED) next_bias = p.bias && n < p.n ? p.bias[n] : 0.0f;
+            next_sa = m < p.m ? p.scale_a[m] : 0.0f;
+        };
+        fetch(first);
         for (int t = first; t < g.tiles; t += step, tl++) {
             const uint32_t b = tl & 1;
             const int m0 = (t % g.tiles_m) * (2 * BM) + (int)rank * BM + 32 * q;
             const int n0 = (t / g.tiles_m) * ROWS;
-            // channel scales of the tile: one a thread (256 epilogue threads, 256 columns)
-            w8::named_barrier(1, 32 * kEpiWarps);   // the last tile's are no longer read
-            {
-                const int c = threadIdx.x - 128;
-                const int n = n0 + (GATED ? c % BNC : c);
-                sh->sw[c] = n < p.n ? (GATED && c >= BNC ? p.scale_1 : p.scale_0)[n] : 0.0f;
-                if (!GATED) sh->bias[c] = p.bias && n < p.n ? p.bias[n] : 0.0f;
-            }
+            w8::named_barrier(1, 32 * kEpiWarps);   // the last tile's scales are no longer read
+            sh->sw[threadIdx.x - 128] = next_sw;
+            if (!GATED) sh->bias[threadIdx.x - 128] = next_bias;
+            const float sa = next_sa;
             w8::named_barrier(1, 32 * kEpiWarps);
-            const float sa = m0 + lane < p.m ? p.scale_a[m0 + lane] : 0.0f;
+            fetch(t + step);
             ok = ok && tc::mbar_wait(&sh->acc_full[b], (tl >> 1) & 1, p.status, abort_flag);
             if (!ok) continue;
             tc::fence_after_sync();
