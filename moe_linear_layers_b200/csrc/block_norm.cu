@@ -953,29 +953,35 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
     return E == 32 ? go(block_norm_team_kernel<1, 32, false>) : go(block_norm_team_kernel<1, 16, false>);
 }
 
-// When there are rows enough for the persistent form, measured against a team a row (us, bf16, every part, persistent /
-// team a row):
-//   H 512: 12000 rows 16.0 / 14.1 (never below 1024)    H 1000: 4800 rows 18.6 / 15.2, 12000 rows 30.1 / 30.4
-//   H 2048: 4800 rows 25.1 / 24.1, 12000 rows 44.8 / 53.6    H 4096: 2400 rows 26.2 / 25.6, 4800 rows 39.7 / 46.3
-//   H 8192: 600 rows 20.8 / 18.0, 1200 rows 28.3 / 30.0, 4800 rows 70 / 102
-//   H 1001 (a value at a time): 1111 rows 12.2 / 7.9, 1600 rows 12.5 / 11.9, 2400 rows 12.8 / 16.4, 9600 rows 39 / 51
-//   H 5001: 900 rows 26 / 48    H 1002 (pairs): 1111 rows 12.0 / 7.3, 9600 rows 40 / 29 (never)
-// So: three rows a team (two above 4096 values); rows of odd width from 12 an SM (4 above 4096 values) on; rows of pairs not at
-// all.  The most values a lane that make up the row, or else leave the lanes four fifths full, cost the fewest instructions.
+// When the persistent form takes the rows.  It issues about half the instructions a value, the team a row moves bytes faster
+// (6.7 against 5.3 TB/s), so it pays where little is moved for much work.  16384 x 2048, persistent / team a row, us:
+//   bf16 in and out (7 bytes a value), codes: 43 / 49; with the norm after the block 51 / 63; with a gate too 53 / 67
+//   the same without codes (8 bytes): 51 / 49     fp32 block output (9 bytes), codes: 55 / 52; with both 58 / 70
+//   fp32 residual (11 bytes), codes: 71 / 59      all fp32 (13 bytes), codes: 85 / 65; with both, no codes 90 / 82
+// Fitted to 16384 x 2048 values, the persistent form's time is 6.3 us a byte and the other's 33 and what is below.
+// It also needs rows enough (bf16 with every part): H 1024, 12000 rows 25.7 / 26.1, 32768 rows 53 / 64; H 2048, 4800 rows 25.1 / 22.6, 12000 rows
+// 44.1 / 50; H 4096, 2400 rows 26.2 / 24.1, 4800 rows 39 / 46; H 8192, 600 rows 20.8 / 17.0, 1200 rows 28 / 30: three rows a
+// team, two above 4096 values, five below 1536.  Rows of odd width (a value at a time): H 1001, 1111 rows 12.2 / 7.0, 1600 rows 12.5 / 11.9, 2400
+// rows 12.8 / 16.4; H 5001, 900 rows 26 / 48: from 12 rows an SM on, 4 above 4096 values; rows of pairs never (H 1002, 9600
+// rows 40 / 29).  The most values a lane that make up the row, or else leave the lanes four fifths full, cost the fewest
+// instructions.
 int launch_many(const Args& a, bool many_gates, cudaStream_t s)
 {
     if (a.H % 2) {
         if (a.H <= 256 || a.T < (a.H > 4096 ? 4 : 12) * q4_num_sms()) return Q4_ERR_UNSUPPORTED;
         return launch_teams(a, a.H <= 512 ? 16 : 32, 0, many_gates, s);
     }
-    if (a.H % 8) return Q4_ERR_UNSUPPORTED;
-    if (a.H < 1024) return Q4_ERR_UNSUPPORTED;
+    if (a.H % 8 || a.H < 1024) return Q4_ERR_UNSUPPORTED;
+    const int bytes = (a.x ? elem_bytes(a.x_dt) : 0) + (a.residual ? elem_bytes(a.r_dt) : 0) + (a.residual_out ? elem_bytes(a.r_dt) : 0) +
+                      (a.y ? elem_bytes(a.y_dt) : 0) + (a.xq ? 1 : 0) + (many_gates ? elem_bytes(a.g_dt) : 0);
+    if (63 * bytes >= 10 * (33 + (a.post_w ? 14 : 0) + (a.gate ? 4 : 0) + (a.xq ? 16 : 0))) return Q4_ERR_UNSUPPORTED;
     // (5120 values: 32 a lane make up the row, 9600 rows 95 us; 64 fill it to five sixths, 104)
     const int full = a.H % 2048 == 0 ? 64 : a.H % 1024 == 0 ? 32 : 0;
-    if (full) return launch_teams(a, full, a.H > 4096 ? 2 : 3, many_gates, s);
+    const int min_rows = a.H > 4096 ? 2 : a.H >= 1536 ? 3 : 5;
+    if (full) return launch_teams(a, full, min_rows, many_gates, s);
     for (int E = 64; E >= 16; E /= 2) {
         const int cap = (a.H + 32 * E - 1) / (32 * E) * 32 * E;
-        if (5 * a.H >= 4 * cap || E == 16) return launch_teams(a, E, a.H > 4096 ? 2 : 3, many_gates, s);
+        if (5 * a.H >= 4 * cap || E == 16) return launch_teams(a, E, min_rows, many_gates, s);
     }
     return Q4_ERR_UNSUPPORTED;
 }
