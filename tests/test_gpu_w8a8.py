@@ -225,6 +225,38 @@ def test_feed_forward_in_sequence(q4):
     assert float(err) < 0.05
 
 
+@pytest.mark.parametrize("m,n,k", [(2, 1024, 1024), (30, 2048, 2048), (150, 1024, 2048), (900, 2048, 1024)])
+def test_buffers_rewritten_in_sequence(q4, m, n, k):
+    """Weights, codes and output buffers that each step rewrites, steps launched back to back: every product reads what
+    the quantizers two launches before it wrote, and none overwrites what an earlier one still reads."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    ws = [(0.05 * torch.randn((n, k), device="cuda", generator=g)).bfloat16() for _ in range(6)]
+    xs = [torch.randn((m, k), device="cuda", generator=g).bfloat16() for _ in range(6)]
+    wq, sw = torch.empty((n, k), dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    xq, sa = torch.empty((m, k), dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    y = torch.empty((m, n), device="cuda")
+
+    def steps(sync):
+        out = []
+        for w, x in zip(ws, xs):
+            q4.act_quant_per_token(w, xq=wq, scale_a=sw)
+            sync()
+            q4.act_quant_per_token(x, xq=xq, scale_a=sa)
+            sync()
+            q4.q8_linear_w8a8(xq, sa, wq, sw, y=y)
+            sync()
+            out.append(y.clone())
+            sync()
+        return out
+
+    want = steps(torch.cuda.synchronize)
+    for _ in range(5):
+        got = steps(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_refusals(q4):
     xq, sa, (w, sw), bias = _inputs(6, 24, 64)
     with pytest.raises(ValueError):
