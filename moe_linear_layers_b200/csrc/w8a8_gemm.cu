@@ -298,8 +298,9 @@ int w8a8_gemm_launch(const Problem& p, cudaStream_t s)
     const bool gated = p.w1 != nullptr;
     CUtensorMap mx, m0, m1, my;
     if (!w8::make_code_map(&mx, p.xq, p.k, p.m, BM) || !w8::make_code_map(&m0, p.w0, p.k, p.n, BNC) ||
-        !w8::make_code_map(&m1, gated ? p.w1 : p.w0, p.k, p.n, BNC))
+        (gated && !w8::make_code_map(&m1, p.w1, p.k, p.n, BNC)))
         return Q4_ERR_CUDA;
+    if (!gated) m1 = m0;
     Grid g;
     g.tiles_m = (p.m + 2 * BM - 1) / (2 * BM);
     const int rows = gated ? BNC : BN;

@@ -200,8 +200,9 @@ int w8a8_split_launch(const Problem& p, int bn, int splits, cudaStream_t s)
     const int rows = gated ? BM / 2 : BM;
     CUtensorMap mx, m0, m1;
     if (!w8::make_code_map(&mx, p.xq, p.k, p.m, bn) || !w8::make_code_map(&m0, p.w0, p.k, p.n, rows) ||
-        !w8::make_code_map(&m1, gated ? p.w1 : p.w0, p.k, p.n, rows))
+        (gated && !w8::make_code_map(&m1, p.w1, p.k, p.n, rows)))
         return Q4_ERR_CUDA;
+    if (!gated) m1 = m0;
     Shape g;
     g.bn = bn;
     g.splits = splits;
