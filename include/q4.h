@@ -272,9 +272,9 @@ int q4_linear_w4a8_ws(const int8_t* xq, const float* scale_a, int32_t m, const q
  *   y[m][n]   = (float(acc) * scale_w[n]) * scale_a[m] + bias[n]            (fp32, each step rounded to nearest)
  * xq [m][k] int8 and scale_a [m] fp32 as act_quant_per_token makes them; wq [n][k] int8 and scale_w [n] fp32 (16-bit
  * weights quantized by the same call: a row of W is one channel); bias [n] fp32 or NULL; y [m][n] fp32 or
- * bf16 (round to nearest even of the fp32 result), overlapping no input.  0 <= m, n <= Q8_MAX_ROWS, 16 <= k <= Q8_MAX_K, k % 16 == 0 (rows start
- * on 16 bytes; Q8_MAX_K is the longest sum of products of -128 .. 127 that int32 holds).  xq, wq and y 16-byte
- * aligned, the fp32 arrays 4-byte aligned.  The result does not depend on how the sum is split: it is exact.
+ * bf16 (round to nearest even of the fp32 result); a y that overlaps an input is refused (Q4_ERR_UNSUPPORTED).
+ * 0 <= m, n <= Q8_MAX_ROWS, 16 <= k <= Q8_MAX_K, k % 16 == 0 (rows start on 16 bytes; Q8_MAX_K is the longest sum of
+ * products of -128 .. 127 that int32 holds).  xq, wq and y 16-byte aligned, the fp32 arrays 4-byte aligned.  The result does not depend on how the sum is split: it is exact.
  * dev_status: Q4_ERR_TIMEOUT when a bounded wait ran out.
  */
 #define Q8_MAX_K 131056

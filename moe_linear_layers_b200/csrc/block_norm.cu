@@ -986,13 +986,6 @@ int launch_many(const Args& a, bool many_gates, cudaStream_t s)
     return Q4_ERR_UNSUPPORTED;
 }
 
-// two arrays share memory (NULL shares none)
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb)
-{
-    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
-    return a && b && p < q + nb && q < p + na;
-}
-
 bool known_dtype(int dt) { return dt == Q4_F32 || dt == Q4_BF16 || dt == Q4_F16; }
 bool aligned_to(const void* p, int dt) { return ((uintptr_t)p & (dt == Q4_F32 ? 3u : 1u)) == 0; }
 
@@ -1027,10 +1020,10 @@ extern "C" int block_norm(const q4_block_norm* d, int32_t T, int32_t H, int32_t*
     for (int o = 0; o < 4; o++) {
         for (int i = 0; i < 5; i++) {
             const bool in_place = o < 2 && i < 2 && out[o] == in[i] && out_n[o] == in_n[i];
-            if (!in_place && overlap(out[o], out_n[o], in[i], in_n[i])) return Q4_ERR_UNSUPPORTED;
+            if (!in_place && q4_overlap(out[o], out_n[o], in[i], in_n[i])) return Q4_ERR_UNSUPPORTED;
         }
         for (int q = 0; q < o; q++)
-            if (overlap(out[o], out_n[o], out[q], out_n[q])) return Q4_ERR_UNSUPPORTED;
+            if (q4_overlap(out[o], out_n[o], out[q], out_n[q])) return Q4_ERR_UNSUPPORTED;
     }
     Args a = {};
     a.x = d->x;

@@ -119,6 +119,13 @@ static inline int q4_launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_
     return q4_cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
+// Whether two arrays share memory (NULL shares none); sizes in bytes.
+static inline bool q4_overlap(const void* a, int64_t na, const void* b, int64_t nb)
+{
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+    return a && b && p < q + nb && q < p + na;
+}
+
 static inline bool q4_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Per-token INT8 quantization of bf16 (f16 = false) or fp16 rows, the kernel behind act_quant_per_token

@@ -73,6 +73,11 @@ int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
     if (!q4_aligned16(p.xq) || !q4_aligned16(p.w0) || !q4_aligned16(p.w1) || !q4_aligned16(p.y) ||
         (((uintptr_t)p.scale_a | (uintptr_t)p.scale_0 | (uintptr_t)p.scale_1 | (uintptr_t)p.bias) & 3u))
         return Q4_ERR_ALIGN;
+    const int64_t m = p.m, n = p.n, ny = m * n * (p.out_bf16 ? 2 : 4);
+    if (q4_overlap(p.y, ny, p.xq, m * p.k) || q4_overlap(p.y, ny, p.w0, n * p.k) || q4_overlap(p.y, ny, p.w1, n * p.k) ||
+        q4_overlap(p.y, ny, p.scale_a, 4 * m) || q4_overlap(p.y, ny, p.scale_0, 4 * n) || q4_overlap(p.y, ny, p.scale_1, 4 * n) ||
+        q4_overlap(p.y, ny, p.bias, 4 * n))
+        return Q4_ERR_UNSUPPORTED;   // tiles are written while others' inputs are still read
     const int64_t groups = (p.m + 15) / 16;
     if (p.m <= 8 || (p.m <= 64 && groups * p.n * p.k * (p.w1 ? 2 : 1) <= (24 << 20))) return w8a8_small_launch(p, s);
     const Choice c = choose(p);

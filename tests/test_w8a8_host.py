@@ -57,6 +57,16 @@ def test_gated_validation(change, expect):
     assert L.q8_linear_w8a8_gated(*a.values(), None, None) == expect
 
 
+@pytest.mark.parametrize("y", ["xq", "scale_a", "wq", "scale_w", "bias"])
+def test_output_over_an_input_is_refused(y):
+    a = dict(xq=1 << 20, scale_a=2 << 20, m=4, wq=3 << 20, scale_w=4 << 20, n=8, k=64, bias=5 << 20)
+    assert L.q8_linear_w8a8(*a.values(), a[y], 0, None, None) == q4.Q4_ERR_UNSUPPORTED
+    assert L.q8_linear_w8a8(*a.values(), a[y] - 64, 0, None, None) == q4.Q4_ERR_UNSUPPORTED   # y is 128 bytes
+    g = (1 << 20, 2 << 20, 4, 3 << 20, 4 << 20, 6 << 20, 7 << 20, 8, 64, 0)
+    for up in (6 << 20, 7 << 20):
+        assert L.q8_linear_w8a8_gated(*g, up, 0, None, None) == q4.Q4_ERR_UNSUPPORTED
+
+
 def test_max_k_is_the_last_exact_sum():
     assert q4.Q8_MAX_K % 16 == 0
     assert 128 * 128 * q4.Q8_MAX_K < 2 ** 31 <= 128 * 128 * (q4.Q8_MAX_K + 16)
