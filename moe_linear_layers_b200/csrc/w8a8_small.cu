@@ -35,10 +35,19 @@ __global__ void __launch_bounds__(kWarps * 32) w8a8_small_kernel(const Problem p
 {
     constexpr int U = MT * MATS == 1 ? 4 : 2;
     __shared__ int part[kWarps][MATS * kRows * 8 * MT];
-    q4_pdl_start();
+    const int n0 = blockIdx.x * kRows, m0 = blockIdx.y * 8 * MT;
+    // The CTA's weight rows (one stretch of memory) start towards L2 while the previous kernel still runs: a prefetch reads
+    // nothing into the kernel, so it may pass the wait.  Weights from DRAM, 1 x 8192 x 2048: 5.0 -> 4.1 us, 1 x 2048 x 8192
+    // 6.7 -> 5.3, gated 1 x 8192 x 2048 8.8 -> 8.9.
+    q4_pdl_trigger();
+    if (threadIdx.x < MATS && blockIdx.y == 0) {
+        const uint32_t bytes = (uint32_t)min(kRows, p.n - n0) * (uint32_t)p.k;
+        const int8_t* w = (threadIdx.x ? p.w1 : p.w0) + (int64_t)n0 * p.k;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w), "r"(bytes) : "memory");
+    }
+    q4_pdl_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int g = lane / 4, t = lane % 4;
-    const int n0 = blockIdx.x * kRows, m0 = blockIdx.y * 8 * MT;
     int acc[MATS][MT][4] = {};
     const int8_t* wr[MATS][2];
     bool wok[2], xok[MT];
