@@ -187,7 +187,7 @@ w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             const float sa = next_sa;
             w8::named_barrier(1, 32 * kEpiWarps);
             fetch(t + step);
-            ok = ok && tc::mbar_wait(&sh->acc_full[b], (tl >> 1) & 1, p.status, abort_flag);
+            ok = ok && w8::warp_wait(&sh->acc_full[b], (tl >> 1) & 1, p.status, abort_flag);
             if (!ok) continue;
             tc::fence_after_sync();
             const uint32_t tcol = tbase + ((uint32_t)(32 * q) << 16) + b * BN;

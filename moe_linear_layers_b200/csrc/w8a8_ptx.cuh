@@ -54,10 +54,15 @@ __device__ __forceinline__ void named_barrier(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// A whole warp's wait: every lane returns the same answer (a lane that gave up takes the others along).
+// A whole warp's wait: every lane returns the same answer, also when a wait gives up just as its phase completes, so what
+// follows may be a whole warp's (TMEM reads, warp barriers).  The vote on every test keeps the warp together: with one vote
+// after per-lane tests, 512 x 8192 x 2048 took 11.03 us against 10.94.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag)
 {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, abort_flag));
+#pragma unroll 1
+    for (int i = 0; i < 64; i++)
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, tc::mbar_wait_slow(bar, parity, status, abort_flag, tc::kWaitLimitNs));
 }
 
 __device__ __forceinline__ void pause_ns(uint64_t ns)

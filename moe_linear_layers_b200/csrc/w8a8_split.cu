@@ -116,9 +116,9 @@ w8a8_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         __syncwarp();
     }
     // every warp: the accumulator is complete, and the ring is free
-    const bool ok = tc::mbar_wait(&sh->acc_full, 0, p.status, nullptr);
+    bool ok = tc::mbar_wait(&sh->acc_full, 0, p.status, nullptr);
     tc::fence_after_sync();
-    __syncthreads();
+    ok = __syncthreads_and(ok);   // (one answer for every lane: the TMEM reads take whole warps)
     if (warp >= 4 && ok) {
         // TMEM lane = weight row, column = token; sums [token][128 rows] in shared memory.  (A CTA without a part of K has zeros.)
         const int q = warp & 3, half = (warp - 4) >> 2;
