@@ -601,6 +601,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // 64 values a lane need 128 registers, fewer fit in 100
 __host__ __device__ constexpr int team_threads(int e) { return e == 64 ? 512 : 640; }
 constexpr int kMaxSlots = 48;   // stages x teams
+constexpr int kTeamSmem = 224 * 1024;   // shared memory a CTA for the vectors and the rings, at most
 
 // A shared vector in fp32: V == 8 keeps the two halves of each 8 values apart, so that a warp's 16-byte reads of
 // consecutive pieces touch every bank once.
@@ -936,13 +937,15 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
     q.gate = vec(a.gate && !many_gates);
     q.pre = vec(a.pre_w);
     q.rings = at;
-    const int room = 224 * 1024 - at;
+    const int room = kTeamSmem - at;
     q.teams = std::min(team_threads(E) / 32 / q.warps, room / row);
     if (q.teams < 1 || a.T < (int64_t)min_rows * sms * q.teams) return Q4_ERR_UNSUPPORTED;
     q.stages = std::min({3, room / (row * q.teams), kMaxSlots / q.teams});
     const int smem = at + q.stages * q.teams * row;
     auto go = [&](auto kern) {
-        if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return q4_cuda_status(e);
+        // the attribute is the kernel's on this device, not the call's: one value for every shape, or a call with a smaller
+        // shape on another thread would lower it between this call's two lines and the launch be refused
+        if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTeamSmem)) return q4_cuda_status(e);
         return q4_launch_pdl(kern, dim3(sms), dim3(team_threads(E)), smem, s, a, q);
     };
     if (full) return E == 64 ? go(block_norm_team_kernel<8, 64, true>) : E == 32 ? go(block_norm_team_kernel<8, 32, true>)
