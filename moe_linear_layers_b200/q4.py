@@ -162,11 +162,27 @@ def _weights_on(device, *weights):
             raise ValueError(f"a weight is on {w.packed.device}, the inputs on {device}")
 
 
+def _empty_for(stream):
+    """torch.empty for the tensors a wrapper makes for a call on `stream` (None: the current one).  The caching allocator
+    hands out memory whose last user may still be queued on the stream it is allocated for, so it is allocated for the
+    stream that writes it first; it is marked in use by the current stream too, where the caller may read it (once
+    ordered) and drop it."""
+    if stream is None:
+        return torch.empty
+
+    def empty(*shape, dtype, device):
+        here = torch.cuda.current_stream(device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(*shape, dtype=dtype, device=device)
+        t.record_stream(here)
+        return t
+    return empty
+
+
 def _hold(stream, *tensors):
     """A call on a stream other than the current one: the caching allocator ties a tensor's memory to the
-    stream it was allocated on, so a workspace or output that this wrapper made (and that may be dropped
-    while the work is still queued) is marked in use by `stream` too, and is not handed out again before
-    that work is done."""
+    stream it was allocated on, so a caller's tensor (which may be dropped while the work is still queued)
+    is marked in use by `stream` too, and is not handed out again before that work is done."""
     if stream is not None:
         for t in tensors:
             if t is not None:
@@ -287,10 +303,11 @@ class Q4Weight:
                         zeros, sum(w.n for w in ws), w0.k, w0.group, w0.symmetric)
 
     @staticmethod
-    def empty(n: int, k: int, group: int, symmetric: bool, device="cuda") -> "Q4Weight":
-        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=device)
-        scales = torch.empty((n, k // group), dtype=torch.float16, device=device)
-        zeros = None if symmetric else torch.empty((n, k // group), dtype=torch.float16, device=device)
+    def empty(n: int, k: int, group: int, symmetric: bool, device="cuda", stream=None) -> "Q4Weight":
+        empty = _empty_for(stream)
+        packed = empty((n, k // 2), dtype=torch.uint8, device=device)
+        scales = empty((n, k // group), dtype=torch.float16, device=device)
+        zeros = None if symmetric else empty((n, k // group), dtype=torch.float16, device=device)
         return Q4Weight(packed, scales, zeros, n, k, group, symmetric)
 
 
@@ -301,7 +318,7 @@ def q4_quantize_pack(w: torch.Tensor, group: int, symmetric: bool, dev_status: t
     n, k = w.shape
     if out is not None and (out.n, out.k, out.group, out.symmetric) != (n, k, group, bool(symmetric)):
         raise ValueError(f"out holds a [{out.n}][{out.k}] group-{out.group} weight, not [{n}][{k}] group-{group}")
-    q = out or Q4Weight.empty(n, k, group, symmetric, device=w.device)
+    q = out or Q4Weight.empty(n, k, group, symmetric, device=w.device, stream=stream)
     _weights_on(w.device, q)
     _hold(stream, q.packed, q.scales, q.zeros)
     _check(_lib.q4_quantize_pack(_ptr(w), n, k, group, int(bool(symmetric)), _ptr(q.packed), _ptr(q.scales),
@@ -312,16 +329,18 @@ def q4_quantize_pack(w: torch.Tensor, group: int, symmetric: bool, dev_status: t
 _SPLIT_WS = {}   # device -> the workspace of split-K GEMMs, grown to the largest size asked for
 
 
-def linear_workspace(m: int, w: Q4Weight, device) -> torch.Tensor | None:
+def linear_workspace(m: int, w: Q4Weight, device, stream=None) -> torch.Tensor | None:
     """A device workspace for q4_linear_w4a16_ws / q4_linear_w4a8_ws at these sizes (None when the shape
     is not split along K), kept per device and grown as needed.  Calls that share it must be ordered on
-    one stream; pass your own to run on several streams at once."""
+    one stream; pass your own to run on several streams at once.  stream: the one the call runs on, where not the current."""
     need = int(_lib.q4_linear_workspace_size(int(m), ctypes.byref(w.desc)))
     if need == 0:
         return None
     ws = _SPLIT_WS.get(device)
     if ws is None or ws.numel() < need:
-        ws = torch.empty((need,), dtype=torch.uint8, device=device)
+        if ws is not None:   # the calls that use the smaller one come before this one
+            ws.record_stream(torch.cuda.current_stream(device) if stream is None else stream)
+        ws = _empty_for(stream)((need,), dtype=torch.uint8, device=device)
         _SPLIT_WS[device] = ws
     return ws
 
@@ -330,16 +349,17 @@ def q4_linear_w4a16(x: torch.Tensor, w: Q4Weight, out_dtype=torch.float32, y: to
                     dev_status: torch.Tensor | None = None, stream=None, workspace="auto") -> torch.Tensor:
     """y[m][n] = x[m][k] . dequant(W)^T; x bf16 CUDA tensor.  workspace: "auto" (the per-device one of
     linear_workspace: a GEMM of few output tiles is split along K), None (never split) or a uint8 tensor."""
+    empty = _empty_for(stream)
     _dev(x, torch.bfloat16, "x")
     _weights_on(x.device, w)
     if x.numel() % w.k:
         raise ValueError(f"x holds {x.numel()} values, not whole rows of k = {w.k}")
     m = x.numel() // w.k
     if y is None:
-        y = torch.empty((m, w.n), dtype=out_dtype, device=x.device)
+        y = empty((m, w.n), dtype=out_dtype, device=x.device)
     od = _out(y, (m, w.n), x.device)
     if isinstance(workspace, str):
-        workspace = linear_workspace(m, w, x.device) if m > q4_linear_w4a16_max_gemv_m() else None
+        workspace = linear_workspace(m, w, x.device, stream) if m > q4_linear_w4a16_max_gemv_m() else None
     if workspace is not None:
         _workspace(workspace, x.device)
     _hold(stream, y, workspace)
@@ -353,6 +373,7 @@ def q4_linear_w4a16_swiglu(gate: torch.Tensor, up: torch.Tensor, w: Q4Weight, ou
                            y: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
     """y[m][n] = h[m][k] . dequant(W)^T with h = silu(gate) * up (fp32 CUDA tensors [m][k], m <= 4)."""
+    empty = _empty_for(stream)
     _dev(gate, torch.float32, "gate")
     _dev(up, torch.float32, "up")
     _weights_on(gate.device, w)
@@ -361,7 +382,7 @@ def q4_linear_w4a16_swiglu(gate: torch.Tensor, up: torch.Tensor, w: Q4Weight, ou
     _numel(up, gate.numel(), "up")
     m = gate.numel() // w.k
     if y is None:
-        y = torch.empty((m, w.n), dtype=out_dtype, device=gate.device)
+        y = empty((m, w.n), dtype=out_dtype, device=gate.device)
     od = _out(y, (m, w.n), gate.device)
     _hold(stream, y)
     _check(_lib.q4_linear_w4a16_swiglu(_ptr(gate), _ptr(up), m, ctypes.byref(w.desc), _ptr(y), od, _ptr(dev_status),
@@ -471,11 +492,12 @@ def q4_linear_w4a16_max_gemv_m() -> int:
 def act_quant_per_token(x: torch.Tensor, xq: torch.Tensor | None = None, scale_a: torch.Tensor | None = None,
                         dev_status: torch.Tensor | None = None, stream=None):
     """Per-token INT8 quantization of a bf16 (or fp16) [m][k] CUDA tensor -> (xq int8 [m][k], scale_a fp32 [m])."""
+    empty = _empty_for(stream)
     f16 = isinstance(x, torch.Tensor) and x.dtype == torch.float16
     _dev(x, torch.float16 if f16 else torch.bfloat16, "x")
     m, k = x.shape
-    xq = torch.empty((m, k), dtype=torch.int8, device=x.device) if xq is None else xq
-    scale_a = torch.empty((m,), dtype=torch.float32, device=x.device) if scale_a is None else scale_a
+    xq = empty((m, k), dtype=torch.int8, device=x.device) if xq is None else xq
+    scale_a = empty((m,), dtype=torch.float32, device=x.device) if scale_a is None else scale_a
     for t, dt, cnt, name in ((xq, torch.int8, m * k, "xq"), (scale_a, torch.float32, m, "scale_a")):
         _numel(_dev(t, dt, name), cnt, name)
         if t.device != x.device:
@@ -492,6 +514,7 @@ def q4_linear_w4a8(xq: torch.Tensor, scale_a: torch.Tensor, w: Q4Weight, out_dty
                    dev_status: torch.Tensor | None = None, stream=None, workspace="auto") -> torch.Tensor:
     """y[m][n] = scale_a[m] * sum_g scale_w[n][g] * (xq . (code - zero))_g; zero = 0 for symmetric W.
     workspace: as q4_linear_w4a16's."""
+    empty = _empty_for(stream)
     _dev(xq, torch.int8, "xq")
     _dev(scale_a, torch.float32, "scale_a")
     _weights_on(xq.device, w)
@@ -504,10 +527,10 @@ def q4_linear_w4a8(xq: torch.Tensor, scale_a: torch.Tensor, w: Q4Weight, out_dty
     if scale_a.device != xq.device or (acc_dbg is not None and acc_dbg.device != xq.device):
         raise ValueError("xq, scale_a and acc_dbg must be on one device")
     if y is None:
-        y = torch.empty((m, w.n), dtype=out_dtype, device=xq.device)
+        y = empty((m, w.n), dtype=out_dtype, device=xq.device)
     od = _out(y, (m, w.n), xq.device)
     if isinstance(workspace, str):
-        workspace = linear_workspace(m, w, xq.device)
+        workspace = linear_workspace(m, w, xq.device, stream)
     if workspace is not None:
         _workspace(workspace, xq.device)
     _hold(stream, y, workspace)
@@ -583,14 +606,14 @@ def _w8_rows(xq, scale_a, wq, name):
     raise ValueError(f"scale_a is on {scale_a.device}, xq on {xq.device}")
 
 
-def _w8_out(y, m, n, out_dtype, xq, name):
+def _w8_out(y, m, n, out_dtype, xq, name, stream):
     """The output of a W8A8 call (made here unless the caller gives it) and its ABI code."""
     if y is not None:
         return y, _out(y, (m, n), xq.device, name)
     if out_dtype is torch.bfloat16:
-        return torch.empty(m, n, dtype=torch.bfloat16, device=xq.device), Q4_OUT_BF16
+        return _empty_for(stream)(m, n, dtype=torch.bfloat16, device=xq.device), Q4_OUT_BF16
     if out_dtype is torch.float32:
-        return torch.empty(m, n, dtype=torch.float32, device=xq.device), Q4_OUT_F32
+        return _empty_for(stream)(m, n, dtype=torch.float32, device=xq.device), Q4_OUT_F32
     raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
 
 
@@ -601,7 +624,7 @@ def q8_linear_w8a8(xq: torch.Tensor, scale_a: torch.Tensor, wq: torch.Tensor, sc
     per-token scales as act_quant_per_token makes them, INT8 weights with one scale per output channel (the
     same call on the rows of a 16-bit weight makes those).  k % 16 == 0; fp32 or bf16 output."""
     m, n, k, dev, xp, sp, wp = _w8_rows(xq, scale_a, wq, "wq")
-    y, od = _w8_out(y, m, n, out_dtype, xq, "y")
+    y, od = _w8_out(y, m, n, out_dtype, xq, "y", stream)
     swp = _same(scale_w, torch.float32, dev, (n,), "scale_w")
     bp = None if bias is None else _same(bias, torch.float32, dev, (n,), "bias")
     st = None if dev_status is None else _status(dev_status, dev)
@@ -626,7 +649,7 @@ def q8_linear_w8a8_gated(xq: torch.Tensor, scale_a: torch.Tensor, wq_gate: torch
     if act not in Q8_ACTS:
         raise ValueError(f"act must be one of {tuple(Q8_ACTS)}, got {act!r}")
     m, n, k, dev, xp, sp, wp = _w8_rows(xq, scale_a, wq_gate, "wq_gate")
-    h, od = _w8_out(h, m, n, out_dtype, xq, "h")
+    h, od = _w8_out(h, m, n, out_dtype, xq, "h", stream)
     sgp = _same(scale_gate, torch.float32, dev, (n,), "scale_gate")
     up, sup = _same(wq_up, torch.int8, dev, (n, k), "wq_up"), _same(scale_up, torch.float32, dev, (n,), "scale_up")
     st = None if dev_status is None else _status(dev_status, dev)
@@ -667,6 +690,7 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
     out_dtype (None unless want_y), and with quant the INT8 codes of n and their per-token scales, amax / 127 (else
     None, None).  residual_out may be residual itself (in place).  fp32, bf16 or fp16 throughout; post_w and pre_w of
     one dtype.  Nothing here has a gradient."""
+    empty = _empty_for(stream)
     lead = x if x is not None else residual
     if not isinstance(lead, torch.Tensor) or not lead.is_cuda or lead.dim() != 2:
         raise TypeError("x (or residual) must be a CUDA tensor [T][H]")
@@ -696,7 +720,7 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
         gp, gd = _norm_rows(gate, (gate_rows, H) if gate.dim() == 2 else (H,), dev, "gate")
     if want_residual:
         if residual_out is None:
-            residual_out = torch.empty(T, H, dtype=r_dtype, device=device)
+            residual_out = empty(T, H, dtype=r_dtype, device=device)
             rop = residual_out.data_ptr()
         else:
             rop = _same(residual_out, r_dtype, dev, shape, "residual_out")
@@ -709,18 +733,18 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
         if yd is None:
             raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
         if want_y:
-            y = torch.empty(T, H, dtype=out_dtype, device=device)
+            y = empty(T, H, dtype=out_dtype, device=device)
             yp = y.data_ptr()
         else:
             y = None
     if quant:
         if xq is None:
-            xq = torch.empty(T, H, dtype=torch.int8, device=device)
+            xq = empty(T, H, dtype=torch.int8, device=device)
             qp = xq.data_ptr()
         else:
             qp = _same(xq, torch.int8, dev, shape, "xq")
         if scale_a is None:
-            scale_a = torch.empty(T, dtype=torch.float32, device=device)
+            scale_a = empty(T, dtype=torch.float32, device=device)
             sp = scale_a.data_ptr()
         else:
             sp = _same(scale_a, torch.float32, dev, (T,), "scale_a")
@@ -762,6 +786,7 @@ def moe_q4_forward(x: torch.Tensor, router_w: torch.Tensor, router_bias: torch.T
     shared (optional) = (gate, up, down) Q4Weight of a shared expert every token passes through.
     a8_mask: bit 0 runs gate/up, bit 1 runs down on per-row INT8 activation codes (W4A8; no shared expert).
     Returns y, or (y, topk_ids, topk_w, perm, offsets, counts) when want_routing."""
+    empty = _empty_for(stream)
     _dev(x, torch.bfloat16, "x")
     _dev(router_w, torch.float32, "router_w")
     T, H = x.shape
@@ -769,22 +794,22 @@ def moe_q4_forward(x: torch.Tensor, router_w: torch.Tensor, router_bias: torch.T
     E = _router(router_w, router_bias, H, dev)
     _weights_on(dev, *experts, *(shared or ()))
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=dev)
+        y = empty((T, H), dtype=out_dtype, device=dev)
     od = _out(y, (T, H), dev)
     I_s = shared[0].n if shared is not None else 0
     ws_bytes = moe_q4_workspace_size(T, H, I, E, topk, I_s, a8_mask)
     if workspace is None:
-        workspace = torch.empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+        workspace = empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
     _workspace(workspace, dev)
     descs = (q4_weight * 3)(*[e.desc for e in experts])
     sdescs = (q4_weight * 3)(*[e.desc for e in shared]) if shared is not None else None
     ids = wts = perm = offs = cnts = None
     if want_routing:
-        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-        wts = torch.empty((T, topk), dtype=torch.float32, device=dev)
-        perm = torch.empty((T * topk,), dtype=torch.int32, device=dev)
-        offs = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-        cnts = torch.empty((E,), dtype=torch.int32, device=dev)
+        ids = empty((T, topk), dtype=torch.int32, device=dev)
+        wts = empty((T, topk), dtype=torch.float32, device=dev)
+        perm = empty((T * topk,), dtype=torch.int32, device=dev)
+        offs = empty((E + 1,), dtype=torch.int32, device=dev)
+        cnts = empty((E,), dtype=torch.int32, device=dev)
     _hold(stream, y, workspace, ids, wts, perm, offs, cnts)
     if a8_mask:
         _check(_lib.moe_q4_forward_a8(_ptr(x), T, H, _ptr(router_w), _ptr(router_bias), E, topk, descs, I, a8_mask,
@@ -808,6 +833,7 @@ def moe_q4_forward_classes(x: torch.Tensor, router_w: torch.Tensor, router_bias:
     """moe_q4_forward with expert classes: class c = experts class_begin[c] .. class_begin[c+1]-1, whose
     (gate, up, down) Q4Weight triple class_experts[c] is stacked over the class's experts and has its own
     group size and symmetry."""
+    empty = _empty_for(stream)
     _dev(x, torch.bfloat16, "x")
     _dev(router_w, torch.float32, "router_w")
     T, H = x.shape
@@ -818,20 +844,20 @@ def moe_q4_forward_classes(x: torch.Tensor, router_w: torch.Tensor, router_bias:
     if len(class_begin) != n + 1:
         raise ValueError("class_begin needs one more entry than there are classes")
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=dev)
+        y = empty((T, H), dtype=out_dtype, device=dev)
     od = _out(y, (T, H), dev)
     if workspace is None:
-        workspace = torch.empty((max(moe_q4_workspace_size(T, H, I, E, topk), 1),), dtype=torch.uint8, device=dev)
+        workspace = empty((max(moe_q4_workspace_size(T, H, I, E, topk), 1),), dtype=torch.uint8, device=dev)
     _workspace(workspace, dev)
     begin = (_i32 * (n + 1))(*[int(v) for v in class_begin])
     descs = (q4_weight * (3 * n))(*[w.desc for trip in class_experts for w in trip])
     ids = wts = perm = offs = cnts = None
     if want_routing:
-        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-        wts = torch.empty((T, topk), dtype=torch.float32, device=dev)
-        perm = torch.empty((T * topk,), dtype=torch.int32, device=dev)
-        offs = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-        cnts = torch.empty((E,), dtype=torch.int32, device=dev)
+        ids = empty((T, topk), dtype=torch.int32, device=dev)
+        wts = empty((T, topk), dtype=torch.float32, device=dev)
+        perm = empty((T * topk,), dtype=torch.int32, device=dev)
+        offs = empty((E + 1,), dtype=torch.int32, device=dev)
+        cnts = empty((E,), dtype=torch.int32, device=dev)
     _hold(stream, y, workspace, ids, wts, perm, offs, cnts)
     _check(_lib.moe_q4_forward_classes(_ptr(x), T, H, _ptr(router_w), _ptr(router_bias), E, topk, n, begin, descs,
                                        I, _ptr(y), od, _ptr(ids), _ptr(wts), _ptr(perm), _ptr(offs), _ptr(cnts),
@@ -848,17 +874,18 @@ def moe_q4_forward_range(x: torch.Tensor, router_w: torch.Tensor, router_bias: t
                          stream=None) -> torch.Tensor:
     """The contribution of experts e_begin .. e_end-1 (weights stacked over that range) to the MoE layer,
     fp32 [T][H]; disjoint ranges covering every expert sum to the layer."""
+    empty = _empty_for(stream)
     _dev(x, torch.bfloat16, "x")
     _dev(router_w, torch.float32, "router_w")
     T, H = x.shape
     E = _router(router_w, router_bias, H, x.device)
     _weights_on(x.device, *experts)
     if y is None:
-        y = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        y = empty((T, H), dtype=torch.float32, device=x.device)
     _dev(y, torch.float32, "y")
     _out(y, (T, H), x.device)
     if workspace is None:
-        workspace = torch.empty((max(moe_q4_workspace_size(T, H, I, E, topk), 1),), dtype=torch.uint8, device=x.device)
+        workspace = empty((max(moe_q4_workspace_size(T, H, I, E, topk), 1),), dtype=torch.uint8, device=x.device)
     _workspace(workspace, x.device)
     descs = (q4_weight * 3)(*[e.desc for e in experts])
     _hold(stream, y, workspace)
@@ -896,13 +923,14 @@ def moe_q4_forward_noalloc(x: torch.Tensor, router_w: torch.Tensor, router_bias:
     that cannot allocate device memory (see include/q4.h).  Sizes needing more than
     Q4_MOE_NOALLOC_SCRATCH_BYTES of scratch raise Q4Error(Q4_ERR_WORKSPACE).  Calls share the scratch:
     keep them ordered on one stream."""
+    empty = _empty_for(stream)
     _dev(x, torch.bfloat16, "x")
     _dev(router_w, torch.float32, "router_w")
     T, H = x.shape
     E = _router(router_w, router_bias, H, x.device)
     _weights_on(x.device, *experts)
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=x.device)
+        y = empty((T, H), dtype=out_dtype, device=x.device)
     od = _out(y, (T, H), x.device)
     descs = (q4_weight * 3)(*[e.desc for e in experts])
     _hold(stream, y)
@@ -922,19 +950,20 @@ def moe_q4_route(x: torch.Tensor, router_w: torch.Tensor, router_bias: torch.Ten
     topk_ids [T][topk] i32, topk_w [T][topk] f32, offsets [E+1] i32, pair_pos [T*topk] i32 (the permuted
     position of each (token, slot) pair), x_perm [T*topk][H] bf16 (the rows in expert order: the dispatch
     buffer), row_expert [T*topk] i32 (the expert of each permuted row)."""
+    empty = _empty_for(stream)
     _dev(x, torch.bfloat16, "x")
     _dev(router_w, torch.float32, "router_w")
     T, H = x.shape
     dev = x.device
     E = _router(router_w, router_bias, H, dev)
     P = T * topk
-    out = {"topk_ids": torch.empty((T, topk), dtype=torch.int32, device=dev),
-           "topk_w": torch.empty((T, topk), dtype=torch.float32, device=dev),
-           "offsets": torch.empty((E + 1,), dtype=torch.int32, device=dev),
-           "pair_pos": torch.empty((P,), dtype=torch.int32, device=dev),
-           "x_perm": torch.empty((P, H), dtype=torch.bfloat16, device=dev),
-           "row_expert": torch.empty((P,), dtype=torch.int32, device=dev)}
-    ws = torch.empty((max(int(_lib.moe_q4_route_workspace_size(T, E, topk)), 1),), dtype=torch.uint8, device=dev)
+    out = {"topk_ids": empty((T, topk), dtype=torch.int32, device=dev),
+           "topk_w": empty((T, topk), dtype=torch.float32, device=dev),
+           "offsets": empty((E + 1,), dtype=torch.int32, device=dev),
+           "pair_pos": empty((P,), dtype=torch.int32, device=dev),
+           "x_perm": empty((P, H), dtype=torch.bfloat16, device=dev),
+           "row_expert": empty((P,), dtype=torch.int32, device=dev)}
+    ws = empty((max(int(_lib.moe_q4_route_workspace_size(T, E, topk)), 1),), dtype=torch.uint8, device=dev)
     _hold(stream, ws, *out.values())
     _check(_lib.moe_q4_route(_ptr(x), T, H, _ptr(router_w), _ptr(router_bias), E, topk, _ptr(out["topk_ids"]),
                              _ptr(out["topk_w"]), _ptr(out["offsets"]), _ptr(out["pair_pos"]), _ptr(out["x_perm"]),
@@ -950,6 +979,7 @@ def moe_q4_forward_rows(x_rows: torch.Tensor, row_expert: torch.Tensor, e_base: 
     """The expert FFN on rows routed elsewhere (moe_q4_forward_rows): y[r] = row_weight[r] *
     FFN_{row_expert[r] - e_base}(x_rows[r]), fp32 [R][H]; experts = (gate, up, down) stacked over the E
     local experts (E = gate.n / I)."""
+    empty = _empty_for(stream)
     _dev(x_rows, torch.bfloat16, "x_rows")
     _dev(row_expert, torch.int32, "row_expert")
     R, H = x_rows.shape
@@ -959,11 +989,11 @@ def moe_q4_forward_rows(x_rows: torch.Tensor, row_expert: torch.Tensor, e_base: 
     if row_weight is not None:
         _numel(_dev(row_weight, torch.float32, "row_weight"), R, "row_weight")
     if y is None:
-        y = torch.empty((R, H), dtype=torch.float32, device=x_rows.device)
+        y = empty((R, H), dtype=torch.float32, device=x_rows.device)
     _dev(y, torch.float32, "y")
     _out(y, (R, H), x_rows.device)
     if workspace is None:
-        workspace = torch.empty((max(int(_lib.moe_q4_rows_workspace_size(R, H, I, E)), 1),), dtype=torch.uint8,
+        workspace = empty((max(int(_lib.moe_q4_rows_workspace_size(R, H, I, E)), 1),), dtype=torch.uint8,
                                 device=x_rows.device)
     _workspace(workspace, x_rows.device)
     descs = (q4_weight * 3)(*[e.desc for e in experts])
@@ -977,6 +1007,7 @@ def moe_q4_forward_rows(x_rows: torch.Tensor, row_expert: torch.Tensor, e_base: 
 def moe_q4_combine(o_rows: torch.Tensor, pair_pos: torch.Tensor, topk_w: torch.Tensor, out_dtype=torch.float32,
                    y: torch.Tensor | None = None, dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j topk_w[t][j] * o_rows[pair_pos[t*topk + j]] (moe_q4_combine), slot order j."""
+    empty = _empty_for(stream)
     _dev(o_rows, torch.float32, "o_rows")
     _dev(pair_pos, torch.int32, "pair_pos")
     _dev(topk_w, torch.float32, "topk_w")
@@ -984,7 +1015,7 @@ def moe_q4_combine(o_rows: torch.Tensor, pair_pos: torch.Tensor, topk_w: torch.T
     T, topk = topk_w.shape
     _numel(pair_pos, T * topk, "pair_pos")
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=o_rows.device)
+        y = empty((T, H), dtype=out_dtype, device=o_rows.device)
     od = _out(y, (T, H), o_rows.device)
     _hold(stream, y)
     _check(_lib.moe_q4_combine(_ptr(o_rows), P, H, _ptr(pair_pos), _ptr(topk_w), T, topk, _ptr(y), od,
