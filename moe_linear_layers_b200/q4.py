@@ -688,9 +688,13 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
     and normed); residual [T][H] (None: r = the gated b); gate None, [H], or [G][H] (each row for T / G consecutive
     tokens).  Returns (r, n, xq, scale_a): r in the residual's dtype (x's without one; None unless want_residual), n in
     out_dtype (None unless want_y), and with quant the INT8 codes of n and their per-token scales, amax / 127 (else
-    None, None).  residual_out may be residual itself (in place).  fp32, bf16 or fp16 throughout; post_w and pre_w of
-    one dtype.  Nothing here has a gradient."""
+    None, None).  An output the caller gives (residual_out, y, xq, scale_a) is written in place of a new one (y's own dtype
+    then counts, not out_dtype); one that the call would not write is refused.  residual_out may be residual itself (in
+    place).  fp32, bf16 or fp16 throughout; post_w and pre_w of one dtype.  Nothing here has a gradient."""
     empty = _empty_for(stream)
+    if ((not quant and (xq is not None or scale_a is not None)) or (y is not None and not want_y)
+            or (residual_out is not None and not want_residual)):
+        raise ValueError("an output is given that the call would not write: xq and scale_a need quant, y want_y, residual_out want_residual")
     lead = x if x is not None else residual
     if not isinstance(lead, torch.Tensor) or not lead.is_cuda or lead.dim() != 2:
         raise TypeError("x (or residual) must be a CUDA tensor [T][H]")
