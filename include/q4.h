@@ -301,6 +301,14 @@ int q8_linear_w8a8_gated(const int8_t* xq, const float* scale_a, int32_t m, cons
                          int32_t act, void* h, int32_t out_dtype, int32_t* dev_status, void* stream);
 
 /*
+ * q8_linear_w8a8_kernel -- the kernel that a product of these sizes (gated: the gated one) takes on the current device: the
+ * streaming one for few tokens, the one that splits K over a cluster, or the one on CTA pairs; Q4_ERR_SHAPE for sizes that
+ * launch nothing.  The outputs do not depend on it (a test hook: the choice rests on measured times).
+ */
+enum { Q8_KERNEL_STREAM = 0, Q8_KERNEL_SPLIT = 1, Q8_KERNEL_PAIR = 2 };
+int q8_linear_w8a8_kernel(int32_t m, int32_t n, int32_t k, int32_t gated);
+
+/*
  * block_norm -- what stands between two blocks of a layer stack, in one pass over the rows: the norm after a
  * block, its gate, the residual update with its scales, the norm before the next block, and the INT8 codes for
  * the next block's first product.

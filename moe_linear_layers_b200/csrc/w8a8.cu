@@ -36,17 +36,19 @@ namespace {
 //   pair:  5.3 + 0.27 a block of K a wave, and 3 more from the second wave on
 // (2048 x 8192, 65 tokens: split 9.2, pair 22.4; 2048 x 2048, 512 tokens: 9.2 / 9.9; 8192 x 2048, 256 tokens: 13.3 / 10.5.)
 struct Choice {
-    int bn, splits;   // bn 0: the pair kernel
+    int kernel;       // Q8_KERNEL_*
+    int bn, splits;   // the split kernel's
 };
 
-Choice choose(const w8::Problem& p)
+Choice choose(const w8::Problem& p, bool gated)
 {
-    const bool gated = p.w1 != nullptr;
+    const int64_t groups = (p.m + 15) / 16;
+    if (p.m <= 8 || (p.m <= 64 && groups * p.n * p.k * (gated ? 2 : 1) <= (24 << 20))) return {Q8_KERNEL_STREAM, 0, 0};
     const int kb = (p.k + 127) / 128, sms = q4_num_sms();
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t pair_waves = ceil_div(ceil_div(p.m, 256) * ceil_div(p.n, gated ? 128 : 256), sms / 2);
     double best = 5.3 + 0.27 * kb * pair_waves + 3.0 * (pair_waves - 1);
-    Choice c = {0, 1};
+    Choice c = {Q8_KERNEL_PAIR, 0, 0};
     const int64_t tiles_n = ceil_div(p.n, gated ? 64 : 128);
     for (int i = 0; i < 4; i++) {
         const int bn = 32 << i;
@@ -57,16 +59,21 @@ Choice choose(const w8::Problem& p)
             const double t = 1.5 + waves * (1.8 + bn / (36.0 * splits) + (splits > 1 ? bn / 128.0 : 0.0) + block[i] * ceil_div(kb, splits));
             if (t < best) {
                 best = t;
-                c = {bn, splits};
+                c = {Q8_KERNEL_SPLIT, bn, splits};
             }
         }
     }
     return c;
 }
 
+bool sizes_ok(int m, int n, int k)
+{
+    return m >= 0 && n >= 0 && m <= Q8_MAX_ROWS && n <= Q8_MAX_ROWS && k >= 16 && k <= Q8_MAX_K && k % 16 == 0;
+}
+
 int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
 {
-    if (p.m < 0 || p.n < 0 || p.m > Q8_MAX_ROWS || p.n > Q8_MAX_ROWS || p.k < 16 || p.k > Q8_MAX_K || p.k % 16) return Q4_ERR_SHAPE;
+    if (!sizes_ok(p.m, p.n, p.k)) return Q4_ERR_SHAPE;
     if (out_dtype != Q4_OUT_F32 && out_dtype != Q4_OUT_BF16) return Q4_ERR_UNSUPPORTED;
     if (p.m == 0 || p.n == 0) return Q4_OK;   // an empty product reads and writes nothing
     if (!p.xq || !p.scale_a || !p.w0 || !p.scale_0 || !p.y || (p.w1 && !p.scale_1)) return Q4_ERR_NULL;
@@ -78,10 +85,10 @@ int run(const w8::Problem& p, int32_t out_dtype, cudaStream_t s)
         q4_overlap(p.y, ny, p.scale_a, 4 * m) || q4_overlap(p.y, ny, p.scale_0, 4 * n) || q4_overlap(p.y, ny, p.scale_1, 4 * n) ||
         q4_overlap(p.y, ny, p.bias, 4 * n))
         return Q4_ERR_UNSUPPORTED;   // tiles are written while others' inputs are still read
-    const int64_t groups = (p.m + 15) / 16;
-    if (p.m <= 8 || (p.m <= 64 && groups * p.n * p.k * (p.w1 ? 2 : 1) <= (24 << 20))) return w8a8_small_launch(p, s);
-    const Choice c = choose(p);
-    return c.bn ? w8a8_split_launch(p, c.bn, c.splits, s) : w8a8_gemm_launch(p, s);
+    const Choice c = choose(p, p.w1 != nullptr);
+    return c.kernel == Q8_KERNEL_STREAM  ? w8a8_small_launch(p, s)
+           : c.kernel == Q8_KERNEL_SPLIT ? w8a8_split_launch(p, c.bn, c.splits, s)
+                                         : w8a8_gemm_launch(p, s);
 }
 
 }  // namespace
@@ -102,4 +109,14 @@ extern "C" int q8_linear_w8a8_gated(const int8_t* xq, const float* scale_a, int3
     if (m > 0 && n > 0 && !wq_up) return Q4_ERR_NULL;
     const w8::Problem p = {xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, nullptr, h, m, n, k, out_dtype == Q4_OUT_BF16, act, dev_status};
     return run(p, out_dtype, (cudaStream_t)stream);
+}
+
+extern "C" int q8_linear_w8a8_kernel(int32_t m, int32_t n, int32_t k, int32_t gated)
+{
+    if (!sizes_ok(m, n, k) || m == 0 || n == 0) return Q4_ERR_SHAPE;
+    w8::Problem p = {};
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    return choose(p, gated != 0).kernel;
 }

@@ -45,7 +45,7 @@ EXPORTED = ("q4_status_string", "q4_version", "q4_build_flags", "q4_last_cuda_er
             "moe_q4_forward_range", "q4_linear_w4a16_chain_sync_bytes", "q4_linear_w4a16_chain",
             "moe_q4_route_workspace_size", "moe_q4_route", "moe_q4_rows_workspace_size", "moe_q4_forward_rows",
             "moe_q4_combine", "q4_linear_workspace_size", "q4_linear_w4a16_ws", "q4_linear_w4a8_ws",
-            "q8_linear_w8a8", "q8_linear_w8a8_gated", "block_norm")
+            "q8_linear_w8a8", "q8_linear_w8a8_gated", "q8_linear_w8a8_kernel", "block_norm")
 Q4_MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -117,6 +117,7 @@ _lib.moe_q4_forward_noalloc.argtypes = [_p, _i32, _i32, _p, _p, _i32, _i32, ctyp
                                         _i32, _p, _p, _p, _p, _p, _p, _p]
 _lib.q8_linear_w8a8.argtypes = [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p]
 _lib.q8_linear_w8a8_gated.argtypes = [_p, _p, _i32, _p, _p, _p, _p, _i32, _i32, _i32, _p, _i32, _p, _p]
+_lib.q8_linear_w8a8_kernel.argtypes = [_i32, _i32, _i32, _i32]
 _lib.block_norm.argtypes = [_p, _i32, _i32, _p, _p]
 # a q4_block_norm from its fields in order, at a sixth of the cost of filling the ctypes structure
 _pack_block_norm = struct.Struct("9Q6id2f").pack
@@ -662,6 +663,14 @@ def q8_linear_w8a8_gated(xq: torch.Tensor, scale_a: torch.Tensor, wq_gate: torch
                    (xp, sp, m, wp, sgp, up, sup, n, k, Q8_ACTS[act], h.data_ptr(), od, st), dev, stream,
                    (h, xq, scale_a, wq_gate, scale_gate, wq_up, scale_up, dev_status))
     return h
+
+
+def q8_linear_w8a8_kernel(m: int, n: int, k: int, gated: bool = False) -> str:
+    """The kernel a W8A8 product of these sizes takes: "stream", "split" or "pair" (for tests; the outputs do not depend on it)."""
+    rc = _lib.q8_linear_w8a8_kernel(m, n, k, int(gated))
+    if rc < 0:
+        _check(rc, "q8_linear_w8a8_kernel")
+    return ("stream", "split", "pair")[rc]
 
 
 _NORM_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}

@@ -137,3 +137,14 @@ def test_binding_refuses_host_tensors_and_unknown_options():
         q4.block_norm(torch.zeros((4, 64)), None, None)
     with pytest.raises(TypeError):
         q4.block_norm(None, None, None)
+
+
+def test_kernel_choice():
+    """Which kernel a size takes (148 SMs: also what the library assumes without a GPU): the three regimes, and sizes that launch
+    nothing."""
+    for m, n, k, want in ((1, 2048, 2048, "stream"), (8, 2048, 8192, "stream"), (200, 1024, 2048, "split"), (333, 1003, 1040, "split"),
+                          (4096, 8192, 2048, "pair"), (2048, 2048, 131056, "pair")):
+        assert q4.q8_linear_w8a8_kernel(m, n, k) == q4.q8_linear_w8a8_kernel(m, n, k, gated=True) == want
+    for sizes in ((0, 8, 64), (8, 0, 64), (8, 8, 24), (8, 8, q4.Q8_MAX_K + 16), (-1, 8, 64)):
+        with pytest.raises(q4.Q4Error):
+            q4.q8_linear_w8a8_kernel(*sizes)
