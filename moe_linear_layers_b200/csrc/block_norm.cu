@@ -207,7 +207,10 @@ template <int V> __device__ __forceinline__ void store_codes(int8_t* p, const fl
     else *p = (int8_t)o[0];
 }
 
-// Rows of more than 16384 values: a CTA of up to 1024 threads a row, V values a load, P loads a thread.
+// Rows of more than 16384 values (where the persistent form does not take them, see launch_many): a CTA of 1024 threads a row, V
+// values a load, P loads a thread.  A thread's 32 values of x and of the residual do not fit its 64 registers: 296 bytes of spill
+// stores with V = 8, 588 with V = 1, and a branch on a type stands at every access.  2048 x 32768 with every part: bf16 223 us, fp32
+// 251 (3.5 TB/s); odd widths, 2048 x 32767: 1016 and 982 us.
 template <int V, int P>
 __global__ void __launch_bounds__(1024) block_norm_wide_kernel(const Args a)
 {
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(512) block_norm_row_kernel(const Args a, const
     });
 }
 
-// Many rows: one persistent CTA of 16 warps an SM.  A team of W warps (1 up to 1024 values a row) owns a row at a time, E
+// Many rows: one persistent CTA of 16 or 20 warps an SM.  A team of W warps (1 up to 2048 values a row) owns a row at a time, E
 // values a lane in registers, so a row's two sums and its maximum cost a lane a few instructions for E values
 // and, with one warp a team, no barrier.  (With 256 threads a row the reductions alone were a fifth of 78 instructions a
 // value: 2.1 TB/s.)  Rows come ahead of use by bulk copies into the team's ring in shared memory: x, the residual, and
@@ -895,7 +898,8 @@ int launch_rows(const Args& a, bool whole, cudaStream_t s)
         return V == 8 ? q4_launch_pdl(block_norm_wide_kernel<8, 4>, grid, block, 0, s, a)
                       : q4_launch_pdl(block_norm_wide_kernel<1, 32>, grid, block, 0, s, a);
     }
-    // values a lane: 8 in rows of up to 256 (and one at a time: 16 take 92 registers), else 16; 16 warps a row at most
+    // values a lane: 8 in rows of up to 256 (and one at a time: 16 take 110 registers, and 32, for rows above 8192 values, spill
+    // 76 bytes), else 16; 16 warps a row at most
     int E = a.H <= 256 || V == 1 ? 8 : 16;
     while (32 * E * 16 < a.H) E *= 2;
     const int W = (a.H + 32 * E - 1) / (32 * E), teams = (8 + W - 1) / W;   // (8 warps a CTA or the next multiple: 2400 x 3000 in 20.0 us with 12 warps, 23.3 with 6)
@@ -952,7 +956,7 @@ int launch_teams(const Args& a, int E, int min_rows, bool many_gates, cudaStream
                                                                                  : go(block_norm_team_kernel<8, 16, true>);
     if (V == 8) return E == 64 ? go(block_norm_team_kernel<8, 64, false>) : E == 32 ? go(block_norm_team_kernel<8, 32, false>)
                                                                                     : go(block_norm_team_kernel<8, 16, false>);
-    if (E == 64) return Q4_ERR_UNSUPPORTED;   // (spills)
+    if (E == 64) return Q4_ERR_UNSUPPORTED;   // (not instantiated: 64 values a lane, one at a time, spilled)
     return E == 32 ? go(block_norm_team_kernel<1, 32, false>) : go(block_norm_team_kernel<1, 16, false>);
 }
 

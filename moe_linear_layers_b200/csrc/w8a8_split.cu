@@ -2,7 +2,7 @@
 //
 // The weights are the MMA's M side here (128 rows a tile; gated: 64 of gate and 64 of up), the tokens its N side (a tile of
 // 32 to 256), so that a batch of any size reads the weights once per token tile and pays for no empty rows of M.  A cluster
-// of up to 8 CTAs shares a tile: CTA r sums its part of K in its own TMEM, the int32 sums go to its shared memory, and each
+// of up to 4 CTAs shares a tile: CTA r sums its part of K in its own TMEM, the int32 sums go to its shared memory, and each
 // CTA then adds up one slice of the tokens over the cluster (distributed shared memory), rescales and stores it.  Integer sums
 // do not depend on the split, so the result is the same for every cluster size, and no workspace is needed.
 //
