@@ -467,9 +467,12 @@ class GemvChain:
         self.y = (_p * self.count)(*[y.data_ptr() for _, _, y in probs])
         nbytes = int(_lib.q4_linear_w4a16_chain_sync_bytes(self.n_stages))
         self.sync = torch.zeros((nbytes // 4,), dtype=torch.int32, device=dev)
+        # zero before any stream's first call, which nothing orders behind this stream (a capture replays in order as it is)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()
 
     def reset(self):
-        """Zero the stage counters (needed only after a call that reported Q4_ERR_TIMEOUT)."""
+        """Zero the stage counters on the current stream (needed only after a call that reported Q4_ERR_TIMEOUT)."""
         self.sync.zero_()
 
     def __call__(self, dev_status: torch.Tensor | None = None, stream=None):

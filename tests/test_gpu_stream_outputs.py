@@ -86,3 +86,27 @@ def test_captured_with_a_forked_stream(q4):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
         del graph
+
+
+def test_chain_built_behind_queued_work(q4):
+    """A chain built while the current stream is busy, called at once on another: its stage counters are zero by then."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn(1024, device="cuda", generator=g).bfloat16()
+    w1, w2 = (q4.q4_quantize_pack(0.05 * torch.randn((1024, 1024), device="cuda", generator=g), 64, True) for _ in range(2))
+    mid, out = torch.empty(1024, dtype=torch.bfloat16, device="cuda"), torch.empty(1024, dtype=torch.bfloat16, device="cuda")
+    stages = [[(x, w1, mid)], [(mid, w2, out)]]
+    q4.GemvChain(stages)()
+    torch.cuda.synchronize()
+    want = out.clone()
+    side = torch.cuda.Stream()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        out.zero_()
+        torch.cuda.synchronize()
+        junk = torch.full((4096,), 7, dtype=torch.int32, device="cuda")   # memory the counters may be given
+        del junk
+        torch.cuda._sleep(10_000_000)
+        q4.GemvChain(stages)(dev_status=st, stream=side)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and torch.equal(out, want)

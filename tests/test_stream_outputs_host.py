@@ -169,3 +169,26 @@ def test_shared_workspace_grows_behind_its_users(made, monkeypatch):
     size[0] = 256
     q4.linear_workspace(16, W["w"], dev)
     assert HERE in b.marks
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_chain_counters_are_zero_before_any_call(made, monkeypatch, capturing):
+    """A chain's stage counters are zeroed on the stream that builds it, and its calls may go to any: the zeros are waited for
+    once, where the chain is built (never inside a capture, which may not wait)."""
+    tensors, lib, W = made
+    waited = []
+
+    class Current:
+        def synchronize(self):
+            waited.append(len(lib.streams))
+
+    monkeypatch.setattr(torch, "zeros", lambda *s, dtype=None, device=None: torch.ones(*s, dtype=dtype).mul(0).as_subclass(Cuda))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Current())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(Library, "q4_linear_w4a16_chain_sync_bytes", lambda self, n: 64, raising=False)
+    w = W["w"]
+    x, y = torch.ones(w.k, dtype=torch.bfloat16).as_subclass(Cuda), torch.ones(w.n).as_subclass(Cuda)
+    chain = q4.GemvChain([[(x, w, y)]])
+    assert waited == ([] if capturing else [0])
+    chain(stream=SIDE)
+    assert lib.streams == [SIDE.cuda_stream] and waited == ([] if capturing else [0])
