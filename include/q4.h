@@ -321,8 +321,10 @@ int q8_linear_w8a8_kernel(int32_t m, int32_t n, int32_t k, int32_t gated);
  *   n  = (r' * rstd(r')) * pre_w         (no factor when pre_w is NULL)
  * Each product and sum above is one fp32 operation rounded to nearest, in that order; r' is rounded to its type
  * only where it is stored (n comes from the fp32 values).  The codes are those of the rows n as y_dtype
- * holds them: scale_a = amax * fp32(1 / 127) (within an ulp of act_quant_per_token's amax / 127, without its division),
- * xq = rne(n / scale_a) with an IEEE division, clamped to [-128, 127]; a row of zeros gets scale 0 and zeros.
+ * holds them: scale_a = amax * fp32(1 / 127), xq = rne(n / scale_a) with an IEEE division, clamped to [-128, 127]; a row of
+ * zeros gets scale 0 and zeros.  The scale is the product that tensor libraries make of a division by a constant on a GPU;
+ * act_quant_per_token's is an IEEE division, within an ulp of it, and its codes of the same row may differ by one where a
+ * quotient lies next to a rounding border.
  *   x [T][H], residual [T][H] (either may be NULL, not both; a gate or post_w needs x);
  *   post_w, pre_w [H] of w_dtype; gate [gate_rows][H]: row t / (T / gate_rows) scales token t (gate_rows divides T;
  *   1: one gate for all); residual_out [T][H] of residual_dtype; y [T][H] of y_dtype; xq [T][H] int8 with

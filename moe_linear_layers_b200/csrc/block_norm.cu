@@ -161,8 +161,10 @@ template <int V> __device__ __forceinline__ void scale_by(float (&v)[V], const f
     for (int j = 0; j < V; j++) v[j] = __fmul_rn(v[j], f[j]);
 }
 
-// amax / 127, from the bits of amax, as a product with the fp32 reciprocal: an IEEE division would stand at the end of a
-// row's chain of reductions.  Off by at most 2^-23 of itself.
+// amax / 127, from the bits of amax, as a product with the fp32 reciprocal.  That is what a division by the constant 127 is in
+// tensor operations on a GPU, so a row quantized by them has these codes and this scale bit for bit; act_quant_per_token divides
+// (IEEE), and where the two scales differ (in about 5 % of rows, by an ulp: each is off by at most 2^-23 of itself) a
+// value whose quotient lies on a rounding border gets the neighbouring code.
 __device__ __forceinline__ float scale_of(uint32_t top) { return __fmul_rn(__uint_as_float(top), 1.0f / 127.0f); }
 
 // v = what y_dt holds of v; the largest magnitude's bits (their order is the magnitudes', NaN on top)

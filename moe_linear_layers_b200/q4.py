@@ -699,8 +699,8 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
     gate * branch_scale * b; n = norm(r) * pre_w.  x: the block's output [T][H] (None: only the residual is scaled
     and normed); residual [T][H] (None: r = the gated b); gate None, [H], or [G][H] (each row for T / G consecutive
     tokens).  Returns (r, n, xq, scale_a): r in the residual's dtype (x's without one; None unless want_residual), n in
-    out_dtype (None unless want_y), and with quant the INT8 codes of n and their per-token scales, amax / 127 (else
-    None, None).  An output the caller gives (residual_out, y, xq, scale_a) is written in place of a new one (y's own dtype
+    out_dtype (None unless want_y), and with quant the INT8 codes of n and their per-token scales, amax * fp32(1 / 127)
+    (what n.abs().amax(-1) / 127 is on a GPU; act_quant_per_token's IEEE division is within an ulp of it) (else None, None).  An output the caller gives (residual_out, y, xq, scale_a) is written in place of a new one (y's own dtype
     then counts, not out_dtype); one that the call would not write is refused.  residual_out may be residual itself (in
     place).  fp32, bf16 or fp16 throughout; post_w and pre_w of one dtype.  Nothing here has a gradient."""
     empty = _empty_for(stream)
