@@ -26,7 +26,8 @@ struct Problem {
 // acc is exact; fp32 rounds it once (to 2^-24), then each factor once
 __device__ __forceinline__ float rescale(int acc, float sw, float sa) { return __fmul_rn(__fmul_rn((float)acc, sw), sa); }
 
-// v / (1 + e^-z).  __expf and __fdividef are within a few fp32 ulp for the |z| whose result is not negligible; z so
+// v / (1 + e^-z).  __expf is within 2 + 1.173 |z| ulp and __fdividef within 2: for z above 0 the exponential's part is small
+// against 1; at z = -20, where the result is 2e-9 of v, it is 25 ulp (1.5e-6 of the result, far below a bf16 step).  z so
 // negative that e^-z leaves fdividef's range (above 2^126) gives 0, off by less than |v| * 2^-126.
 __device__ __forceinline__ float logistic_times(float v, float z) { return __fdividef(v, 1.0f + __expf(-z)); }
 
