@@ -614,10 +614,11 @@ def _w8_out(y, m, n, out_dtype, xq, name, stream):
     """The output of a W8A8 call (made here unless the caller gives it) and its ABI code."""
     if y is not None:
         return y, _out(y, (m, n), xq.device, name)
+    empty = torch.empty if stream is None else _empty_for(stream)
     if out_dtype is torch.bfloat16:
-        return _empty_for(stream)(m, n, dtype=torch.bfloat16, device=xq.device), Q4_OUT_BF16
+        return empty(m, n, dtype=torch.bfloat16, device=xq.device), Q4_OUT_BF16
     if out_dtype is torch.float32:
-        return _empty_for(stream)(m, n, dtype=torch.float32, device=xq.device), Q4_OUT_F32
+        return empty(m, n, dtype=torch.float32, device=xq.device), Q4_OUT_F32
     raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
 
 
@@ -699,11 +700,12 @@ def block_norm(x: torch.Tensor | None, residual: torch.Tensor | None, pre_w: tor
     gate * branch_scale * b; n = norm(r) * pre_w.  x: the block's output [T][H] (None: only the residual is scaled
     and normed); residual [T][H] (None: r = the gated b); gate None, [H], or [G][H] (each row for T / G consecutive
     tokens).  Returns (r, n, xq, scale_a): r in the residual's dtype (x's without one; None unless want_residual), n in
-    out_dtype (None unless want_y), and with quant the INT8 codes of n and their per-token scales, amax * fp32(1 / 127)
-    (what n.abs().amax(-1) / 127 is on a GPU; act_quant_per_token's IEEE division is within an ulp of it) (else None, None).  An output the caller gives (residual_out, y, xq, scale_a) is written in place of a new one (y's own dtype
+    out_dtype (None unless want_y), and with quant (else None, None) the INT8 codes of n and their per-token scales,
+    amax * fp32(1 / 127): what n.abs().amax(-1) / 127 is on a GPU, and within an ulp of act_quant_per_token's IEEE
+    division.  An output the caller gives (residual_out, y, xq, scale_a) is written in place of a new one (y's own dtype
     then counts, not out_dtype); one that the call would not write is refused.  residual_out may be residual itself (in
     place).  fp32, bf16 or fp16 throughout; post_w and pre_w of one dtype.  Nothing here has a gradient."""
-    empty = _empty_for(stream)
+    empty = torch.empty if stream is None else _empty_for(stream)
     if ((not quant and (xq is not None or scale_a is not None)) or (y is not None and not want_y)
             or (residual_out is not None and not want_residual)):
         raise ValueError("an output is given that the call would not write: xq and scale_a need quant, y want_y, residual_out want_residual")
