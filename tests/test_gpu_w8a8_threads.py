@@ -7,7 +7,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 # pairs of block-norm shapes that one kernel instance of the persistent form serves with different amounts of shared memory:
-# 1 and 8 warps a row of whole 2048s, of other widths of 16-byte rows, and of odd widths
+# rows of whole 2048s, of other widths on 16 bytes, and of odd widths; one warp a row and 8 (odd: 16)
 PAIRS = [((7200, 2048), (600, 16384)), ((7200, 2000), (600, 15000)), ((1800, 1001), (600, 16383))]
 
 
